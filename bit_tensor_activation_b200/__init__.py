@@ -11,6 +11,10 @@ Shapes (P ranks, T rows, H features, k kept features, H' = H - k):
   x [P, T, H] bf16; ema_min/ema_max [P, H] f32; keep_idx [k] i32; rest_idx [H'] i32;
   scale/inv_scale [P, H] f32; zero [P, H] u8; codes [P, T, H'/8] i32 (bit pattern of uint32);
   side [P, k, T] bf16 (feature-major); out [T, H] bf16 or f32.
+
+Around the path, a row-parallel layer in 8-bit integers: hq_quantize_tokens, hq_int8_matmul (the
+partial sums), hq_int8_matmul_pack (the same leaving as the wire) and hq_residual_norm (the end of
+the block after the sum).  These four also take tensors of another device than the current one.
 """
 from __future__ import annotations
 
@@ -62,17 +66,28 @@ for _f in ("hq_calibrate_ld", "hq_quantize_pack_ld", "hq_dequant_reduce_ld", "hq
     getattr(_lib, _f).restype = _i32
 _lib.hq_selftest_set_pipeline_stall.argtypes = [ctypes.c_longlong, ctypes.c_longlong]
 _lib.hq_selftest_set_pipeline_stall.restype = _i32
+_lib.hq_quantize_tokens.argtypes = [_vp, _i32, ctypes.c_int64, _i32, _vp, _i32, _vp, _vp]
+_lib.hq_int8_matmul.argtypes = [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _vp]
+_lib.hq_int8_matmul_pack.argtypes = [_vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                     _vp, _vp, _vp]
+_lib.hq_residual_norm.argtypes = [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _f32, _f32, _i32,
+                                  _vp, _vp, _f32, _vp, _vp, _i32, _vp, _vp]
+for _f in ("hq_quantize_tokens", "hq_int8_matmul", "hq_int8_matmul_pack", "hq_residual_norm"):
+    getattr(_lib, _f).restype = _i32
 _lib.hq_wire_bytes_per_row.argtypes = [_i32, _i32]
 _lib.hq_wire_bytes_per_row.restype = ctypes.c_int64
 
 HQ_OK, HQ_ERR_INVALID_ARG, HQ_ERR_MISALIGNED, HQ_ERR_CUDA, HQ_ERR_TIMEOUT, HQ_ERR_BAD_INDEX = range(6)
 HQ_OUT_BF16, HQ_OUT_F32 = 0, 1
+HQ_NORM_NONE, HQ_NORM_RMS, HQ_NORM_LAYER = 0, 1, 2
+HQ_INT8_MAX_K, HQ_INT8_MAX_H = 65536, 1048576
 
 EXPORTS = ["hq_calibrate", "hq_select_topk", "hq_quantize_pack", "hq_dequant_reduce",
            "hq_dequant_reduce_bf16_shards", "hq_compress_reduce", "hq_status_string", "hq_read_device_error", "hq_wire_bytes_per_row",
            "hq_selftest_bounded_wait", "hq_selftest_set_pipeline_stall", "hq_calibrate_ld", "hq_quantize_pack_ld",
            "hq_dequant_reduce_ld", "hq_compress_reduce_ld", "hq_dequant_reduce_ranks", "hq_two_step_reduce",
-           "hq_two_step_workspace_bytes", "hq_two_step_reduce_noalloc"]
+           "hq_two_step_workspace_bytes", "hq_two_step_reduce_noalloc", "hq_quantize_tokens", "hq_int8_matmul",
+           "hq_int8_matmul_pack", "hq_residual_norm"]
 
 
 class HQError(RuntimeError):
@@ -320,6 +335,123 @@ def hq_compress_reduce_ld(x, keep_idx, rest_idx, scale, inv_scale, zero, out, co
             _ptr(codes, _CODES, (P, T, (H - k) // 8), "codes"), _ptr(side, _BF16, (P, k, T), "side"),
             _stream(stream, x.device))
     _check(_lib.hq_compress_reduce_ld(*args), "hq_compress_reduce_ld")
+
+
+# -- a row-parallel layer in 8-bit integers around the path --------------------------------------
+_I8 = (torch.int8,)
+
+
+def _call(fn, where, device, others, args, stream):
+    """One call of the library on `device`, where every tensor lies, whatever device is current."""
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"{where}: tensors on {device} and {t.device}")
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(stream, device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(stream, device))
+    if st != HQ_OK:
+        raise HQError(st, where)
+
+
+def _pitched(t, dtypes, shape, multiple, name):
+    """(pointer, row pitch in elements) of a tensor [..., n] whose rows are dense and one pitch apart.
+    The strides of dimensions of one element do not count; a tensor of at most one row has the pitch
+    of its width rounded up to `multiple`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.numel():
+        return None, -(-shape[-1] // multiple) * multiple
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: rows must be dense")
+    ld, rows = None, 1
+    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n > 1:
+            if ld is None:
+                ld = s
+            elif s != rows * ld:
+                raise ValueError(f"{name}: rows must be one pitch apart")
+            rows *= n
+    return t.data_ptr(), -(-shape[-1] // multiple) * multiple if ld is None else ld
+
+
+def hq_quantize_tokens(x, q, scale, stream=None) -> None:
+    """x [..., K] bf16 to int8 q [..., K] with one scale a row, scale [...] f32; the rows of x and q
+    may be further apart than K (multiples of 8 and 16 elements)."""
+    *lead, K = x.shape
+    rows = 1
+    for n in lead:
+        rows *= n
+    px, ldx = _pitched(x, _BF16, (*lead, K), 8, "x")
+    pq, ldq = _pitched(q, _I8, (*lead, K), 16, "q")
+    _call(_lib.hq_quantize_tokens, "hq_quantize_tokens", x.device, (q, scale),
+          (px, ldx, rows, K, pq, ldq, _ptr(scale, _F32, tuple(lead), "scale")), stream)
+
+
+def hq_int8_matmul(a, a_scale, w, w_scale, out, bias=None, stream=None) -> None:
+    """Every rank's partial sum out [P, T, H] (bf16 or f32) of int8 activations a [P, T, K] with a
+    scale a token (a_scale [P, T]) and int8 weights w [P, H, K] with a scale a channel (w_scale
+    [P, H]); bias [P, H] bf16.  The rows of a, w and out may be further apart than K and H."""
+    P, T, K = a.shape
+    H = w.shape[1]
+    pa, lda = _pitched(a, _I8, (P, T, K), 16, "a")
+    pw, ldw = _pitched(w, _I8, (P, H, K), 16, "w")
+    po, ldo = _pitched(out, _BF16 + _F32, (P, T, H), 8, "out")
+    _call(_lib.hq_int8_matmul, "hq_int8_matmul", a.device, (a_scale, w, w_scale, bias, out),
+          (pa, lda, _ptr(a_scale, _F32, (P, T), "a_scale"), pw, ldw, _ptr(w_scale, _F32, (P, H), "w_scale"),
+           _ptr(bias, _BF16, (P, H), "bias"), P, T, H, K, po, ldo,
+           HQ_OUT_F32 if out.dtype == torch.float32 else HQ_OUT_BF16), stream)
+
+
+def hq_int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, zero, codes, side,
+                        stream=None) -> None:
+    """The wire (codes, side) of the partial sums that hq_int8_matmul would write, bit for bit as
+    hq_quantize_pack makes it.  w and w_scale have their rows in the wire's order:
+    torch.cat([rest_idx, keep_idx]) of the features' own."""
+    P, T, K = a.shape
+    H = w.shape[1]
+    k = keep_idx.shape[0]
+    pa, lda = _pitched(a, _I8, (P, T, K), 16, "a")
+    pw, ldw = _pitched(w, _I8, (P, H, K), 16, "w")
+    _call(_lib.hq_int8_matmul_pack, "hq_int8_matmul_pack", a.device,
+          (a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, zero, codes, side),
+          (pa, lda, _ptr(a_scale, _F32, (P, T), "a_scale"), pw, ldw, _ptr(w_scale, _F32, (P, H), "w_scale"), P, T, H, K,
+           k, _ptr(keep_idx, _I32, (k,), "keep_idx"), _ptr(rest_idx, _I32, (H - k,), "rest_idx"),
+           _ptr(inv_scale, _F32, (P, H), "inv_scale"), _ptr(zero, _U8, (P, H), "zero"),
+           _ptr(codes, _CODES, (P, T, (H - k) // 8), "codes"), _ptr(side, _BF16, (P, k, T), "side")), stream)
+
+
+def hq_residual_norm(y, res, res_out, h=None, q=None, q_scale=None, post=HQ_NORM_NONE, post_w=None, post_b=None,
+                     gate=None, alpha: float = 1.0, beta: float = 1.0, pre=HQ_NORM_RMS, pre_w=None, pre_b=None,
+                     eps: float = 1e-6, stream=None) -> None:
+    """res_out = alpha * res + beta * gate * norm_post(y), and the norm of res_out as bf16 (h) and/or
+    int8 with one scale a row (q, q_scale).  y, res, res_out, h [T, H] (y and res bf16 or f32; res_out
+    of res's type, res itself allowed); q [T, H] int8, rows may be further apart; weights and biases
+    [H] f32; gate [G, H] bf16 with G a divisor of T: row t uses gate row t // (T // G)."""
+    T, H = y.shape
+    gate_rows = 0
+    if gate is not None:
+        G = gate.shape[0]
+        if G < 1 or T % G:
+            raise ValueError(f"gate: {G} rows do not divide {T}")
+        gate_rows = max(T // G, 1)
+    if res.dtype != res_out.dtype and torch.float32 in (res.dtype, res_out.dtype):
+        raise TypeError("res and res_out must have the same type")
+    pq, ldq = (None, 0) if q is None else _pitched(q, _I8, (T, H), 16, "q")
+    _call(_lib.hq_residual_norm, "hq_residual_norm", y.device,
+          (res, res_out, h, q, q_scale, post_w, post_b, gate, pre_w, pre_b),
+          (_ptr(y, _BF16 + _F32, (T, H), "y"), HQ_OUT_F32 if y.dtype == torch.float32 else HQ_OUT_BF16,
+           _ptr(res, _BF16 + _F32, (T, H), "res"), _ptr(res_out, _BF16 + _F32, (T, H), "res_out"),
+           HQ_OUT_F32 if res.dtype == torch.float32 else HQ_OUT_BF16, T, H, post, _ptr(post_w, _F32, (H,), "post_w"),
+           _ptr(post_b, _F32, (H,), "post_b"), None if gate is None else _ptr(gate, _BF16, (G, H), "gate"), gate_rows,
+           float(alpha), float(beta), pre, _ptr(pre_w, _F32, (H,), "pre_w"), _ptr(pre_b, _F32, (H,), "pre_b"),
+           float(eps), _ptr(h, _BF16, (T, H), "h"), pq, ldq, _ptr(q_scale, _F32, (T,), "q_scale")), stream)
 
 
 def hq_selftest_bounded_wait(limit_cycles: int, stream=None, device=None) -> None:

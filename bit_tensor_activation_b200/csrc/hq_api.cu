@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <type_traits>
 #include <mutex>
@@ -20,8 +21,11 @@
 #include "k_calibrate.cuh"
 #include "k_dequant.cuh"
 #include "k_fused.cuh"
+#include "k_int8mm.cuh"
+#include "k_norm.cuh"
 #include "k_quantize.cuh"
 #include "k_select.cuh"
+#include "k_tokens.cuh"
 
 namespace {
 
@@ -492,6 +496,79 @@ hq_status two_step_entry(const uint16_t* x, int P, int T, int H, int k, const in
   return launch_dequant<float, false>(src, 1, Tb, H, k2, keep2, scale2, zero2, out, H, (cudaStream_t)stream, *d, P);
 }
 
+// A row of n elements over threads: vectors of 8 a thread (NV) and threads a row; 32 threads: a warp
+// to a row, four rows to a CTA.
+struct RowShape {
+  int nv, threads;
+  bool warp;
+};
+RowShape row_shape(int n) {
+  const int nvec = (int)ceil_div(n, 8);
+  if (nvec <= 4 * 32) return RowShape{nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, 128, true};
+  const int nv = nvec <= hq::kRowMaxThreads ? 1 : nvec <= 2 * hq::kRowMaxThreads ? 2 : nvec <= 4 * hq::kRowMaxThreads ? 4 : 8;
+  return RowShape{nv, (int)(32 * ceil_div(ceil_div(nvec, nv), 32)), false};
+}
+
+hq_status quantize_tokens_entry(const uint16_t* x, int ldx, int64_t rows, int K, int8_t* q, int ldq, float* scale,
+                                void* stream) {
+  if (rows < 0 || K < 1 || K > HQ_INT8_MAX_K || !ld_ok(ldx, K) || ldq < K || ldq % 16 != 0) return HQ_ERR_INVALID_ARG;
+  if (rows > 0x7FFFFFFFLL) return HQ_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !q || !scale)) return HQ_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return HQ_ERR_MISALIGNED;
+  if (rows == 0) return HQ_OK;
+  const RowShape s = row_shape(K);
+  const unsigned grid = (unsigned)(s.warp ? ceil_div(rows, 4) : rows);
+  cudaStream_t st = (cudaStream_t)stream;
+#define HQ_ROWS(NV, W) hq::quantize_tokens_kernel<NV, W><<<grid, s.threads, 0, st>>>(x, ldx, rows, K, q, ldq, scale)
+  if (s.warp) {
+    if (s.nv == 1) HQ_ROWS(1, true);
+    else if (s.nv == 2) HQ_ROWS(2, true);
+    else HQ_ROWS(4, true);
+  } else {
+    if (s.nv == 1) HQ_ROWS(1, false);
+    else if (s.nv == 2) HQ_ROWS(2, false);
+    else if (s.nv == 4) HQ_ROWS(4, false);
+    else HQ_ROWS(8, false);
+  }
+#undef HQ_ROWS
+  return launched();
+}
+
+// The checks that the two products share.
+hq_status matmul_check(const int8_t* a, int lda, const float* a_scale, const int8_t* w, int ldw, const float* w_scale,
+                       int P, int T, int H, int max_h, int K) {
+  if (P < 1 || P > kMaxRanks || T < 0 || H < 8 || H > max_h || H % 8 != 0) return HQ_ERR_INVALID_ARG;
+  if (K < 1 || K > HQ_INT8_MAX_K || lda < K || lda % 16 != 0 || ldw < K || ldw % 16 != 0) return HQ_ERR_INVALID_ARG;
+  if (!w || !w_scale || (T > 0 && (!a || !a_scale))) return HQ_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(w_scale, 16) || !aligned(a_scale, 4)) return HQ_ERR_MISALIGNED;
+  return HQ_OK;
+}
+
+template <int kOut>
+hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
+  const dim3 grid((unsigned)ceil_div(p.H, hq::kMmSimpleTile), (unsigned)ceil_div(p.T, hq::kMmSimpleTile), (unsigned)p.P);
+  hq::int8_matmul_simple_kernel<kOut><<<grid, 256, 0, st>>>(p);
+  return launched();
+}
+
+template <typename Y, typename R>
+hq_status launch_norm(const hq::NormArgs& a, cudaStream_t st) {
+  const RowShape s = row_shape(a.H);
+  const unsigned grid = (unsigned)(s.warp ? ceil_div(a.T, 4) : a.T);
+#define HQ_ROWS(NV, W) hq::residual_norm_kernel<Y, R, NV, W><<<grid, s.threads, 0, st>>>(a)
+  if (s.warp) {
+    if (s.nv == 1) HQ_ROWS(1, true);
+    else if (s.nv == 2) HQ_ROWS(2, true);
+    else HQ_ROWS(4, true);
+  } else {
+    if (s.nv == 1) HQ_ROWS(1, false);
+    else if (s.nv == 2) HQ_ROWS(2, false);
+    else HQ_ROWS(4, false);
+  }
+#undef HQ_ROWS
+  return launched();
+}
+
 // Scratch of hq_two_step_reduce_noalloc: a fixed array in every device's global memory, so that a
 // caller that may not allocate device memory needs no workspace.  In host code the array's name
 // only stands for it; its device address is fetched once per device (device_scratch) and passed to
@@ -638,6 +715,73 @@ hq_status hq_compress_reduce_ld(const uint16_t* x, int ldx, int P, int T, int H,
                                 uint32_t* codes_or_null, uint16_t* side_or_null, void* stream) {
   return compress_entry(x, ldx, P, T, H, k, keep_idx, rest_idx, scale, inv_scale, zero, out, ldo, out_dtype,
                         codes_or_null, side_or_null, stream);
+}
+
+hq_status hq_quantize_tokens(const uint16_t* x, int ldx, int64_t rows, int K, int8_t* q, int ldq, float* scale,
+                             void* stream) {
+  return quantize_tokens_entry(x, ldx, rows, K, q, ldq, scale, stream);
+}
+
+hq_status hq_int8_matmul(const int8_t* a, int lda, const float* a_scale, const int8_t* w, int ldw,
+                         const float* w_scale, const uint16_t* bias_or_null, int P, int T, int H, int K, void* out,
+                         int ldo, hq_out_dtype out_dtype, void* stream) {
+  const hq_status c = matmul_check(a, lda, a_scale, w, ldw, w_scale, P, T, H, HQ_INT8_MAX_H, K);
+  if (c == HQ_ERR_INVALID_ARG || !ld_ok(ldo, H) || (T > 0 && !out)) return HQ_ERR_INVALID_ARG;
+  if (out_dtype != HQ_OUT_BF16 && out_dtype != HQ_OUT_F32) return HQ_ERR_INVALID_ARG;
+  if (c != HQ_OK || !aligned(bias_or_null, 16) || !aligned(out, 16)) return HQ_ERR_MISALIGNED;
+  if (T == 0) return HQ_OK;
+  hq::MmArgs p{};
+  p.a = a, p.lda = lda, p.a_scale = a_scale, p.w = w, p.ldw = ldw, p.w_scale = w_scale;
+  p.P = P, p.T = T, p.H = H, p.K = K;
+  p.bias = bias_or_null, p.out = out, p.ldo = ldo;
+  if (out_dtype == HQ_OUT_BF16) return launch_matmul<hq::kMmBf16>(p, (cudaStream_t)stream);
+  return launch_matmul<hq::kMmF32>(p, (cudaStream_t)stream);
+}
+
+hq_status hq_int8_matmul_pack(const int8_t* a, int lda, const float* a_scale, const int8_t* w, int ldw,
+                              const float* w_scale, int P, int T, int H, int K, int k, const int32_t* keep_idx,
+                              const int32_t* rest_idx, const float* inv_scale, const uint8_t* zero, uint32_t* codes,
+                              uint16_t* side, void* stream) {
+  const hq_status c = matmul_check(a, lda, a_scale, w, ldw, w_scale, P, T, H, hq::kMaxH, K);
+  if (c == HQ_ERR_INVALID_ARG || check_shape(P, H, k) != HQ_OK) return HQ_ERR_INVALID_ARG;
+  if (!inv_scale || !zero || (k > 0 && !keep_idx) || (k < H && !rest_idx)) return HQ_ERR_INVALID_ARG;
+  if (T > 0 && ((k > 0 && !side) || (k < H && !codes))) return HQ_ERR_INVALID_ARG;
+  if (c != HQ_OK || !aligned(inv_scale, 16) || !aligned(zero, 16) || !aligned(keep_idx, 4) || !aligned(rest_idx, 4) ||
+      !aligned(side, 16) || !aligned(codes, 4))
+    return HQ_ERR_MISALIGNED;
+  if (T == 0) return HQ_OK;
+  hq::MmArgs p{};
+  p.a = a, p.lda = lda, p.a_scale = a_scale, p.w = w, p.ldw = ldw, p.w_scale = w_scale;
+  p.P = P, p.T = T, p.H = H, p.K = K;
+  p.k = k, p.rest_idx = rest_idx, p.inv_scale = inv_scale, p.zero = zero, p.codes = codes, p.side = side;
+  return launch_matmul<hq::kMmWire>(p, (cudaStream_t)stream);
+}
+
+hq_status hq_residual_norm(const void* y, hq_out_dtype y_dtype, const void* res, void* res_out,
+                           hq_out_dtype res_dtype, int T, int H, hq_norm_kind post, const float* post_w,
+                           const float* post_b, const uint16_t* gate, int gate_rows, float alpha, float beta,
+                           hq_norm_kind pre, const float* pre_w, const float* pre_b, float eps, uint16_t* h, int8_t* q,
+                           int ldq, float* q_scale, void* stream) {
+  if (T < 0 || check_shape(1, H, 0) != HQ_OK) return HQ_ERR_INVALID_ARG;
+  if ((y_dtype != HQ_OUT_BF16 && y_dtype != HQ_OUT_F32) || (res_dtype != HQ_OUT_BF16 && res_dtype != HQ_OUT_F32))
+    return HQ_ERR_INVALID_ARG;
+  if (post < HQ_NORM_NONE || post > HQ_NORM_LAYER || pre < HQ_NORM_NONE || pre > HQ_NORM_LAYER) return HQ_ERR_INVALID_ARG;
+  if (!std::isfinite(alpha) || !std::isfinite(beta) || !(eps >= 0.0f) || !std::isfinite(eps)) return HQ_ERR_INVALID_ARG;
+  if (gate && gate_rows < 1) return HQ_ERR_INVALID_ARG;
+  if (!q != !q_scale || (q && (ldq < H || ldq % 16 != 0))) return HQ_ERR_INVALID_ARG;
+  if (pre == HQ_NORM_NONE && (h || q)) return HQ_ERR_INVALID_ARG;
+  if (T > 0 && (!y || !res || !res_out || (pre != HQ_NORM_NONE && !h && !q))) return HQ_ERR_INVALID_ARG;
+  if (!aligned(y, 16) || !aligned(res, 16) || !aligned(res_out, 16) || !aligned(post_w, 16) || !aligned(post_b, 16) ||
+      !aligned(gate, 16) || !aligned(pre_w, 16) || !aligned(pre_b, 16) || !aligned(h, 16) || !aligned(q, 16) ||
+      !aligned(q_scale, 4))
+    return HQ_ERR_MISALIGNED;
+  if (T == 0) return HQ_OK;
+  hq::NormArgs a{y, res, res_out, T, H, (int)post, (int)pre, post_w, post_b, gate, gate ? gate_rows : 1, alpha, beta,
+                 pre_w, pre_b, eps, h, q, ldq, q_scale};
+  cudaStream_t st = (cudaStream_t)stream;
+  if (y_dtype == HQ_OUT_BF16)
+    return res_dtype == HQ_OUT_BF16 ? launch_norm<uint16_t, uint16_t>(a, st) : launch_norm<uint16_t, float>(a, st);
+  return res_dtype == HQ_OUT_BF16 ? launch_norm<float, uint16_t>(a, st) : launch_norm<float, float>(a, st);
 }
 
 const char* hq_status_string(hq_status s) {

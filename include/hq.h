@@ -261,6 +261,94 @@ hq_status hq_two_step_reduce_noalloc(const uint16_t* x, int P, int T, int H, int
                                      const float* scale2, const float* inv_scale2, const uint8_t* zero2, void* out,
                                      hq_out_dtype out_dtype, void* stream);
 
+/*
+ * A row-parallel layer in 8-bit integers around the path above: what makes the partial sums, and
+ * what follows their sum.  The pages give no arithmetic for either (sections "The Challenge of
+ * Quantization" and "Combating Quantization Errors with Tensor Parallelism" place the compressed
+ * sum behind a row-parallel product); the readings R23..R25 are stated here.
+ *
+ * hq_quantize_tokens (R23): rows of bf16 to int8 with one scale a row.  For row t with
+ * amax = max_k |x[t][k]|:
+ *   scale[t] = amax / 127                      (one fp32 division)
+ *   q[t][k]  = rint(127 * x[t][k] / amax)      of the exact quotient, half to even: -127 .. 127
+ *   a row whose scale would be 0 or subnormal (all zeros among them): scale[t] = 1, q = 0;
+ *   a row that holds an infinity or a NaN: scale[t] = NaN, q = 0, so that every product with the
+ *   row is NaN.
+ *   x      bf16 [rows][K], rows ldx elements apart
+ *   q      int8 [rows][K], rows ldq bytes apart; bytes between K and ldq are left as they are
+ *   scale  float [rows]
+ *   rows >= 0 (0 enqueues nothing); 1 <= K <= HQ_INT8_MAX_K; ldx >= K, a multiple of 8; ldq >= K, a
+ *   multiple of 16; x and q 16-byte aligned.
+ */
+#define HQ_INT8_MAX_K 65536
+#define HQ_INT8_MAX_H 1048576
+hq_status hq_quantize_tokens(const uint16_t* x, int ldx, int64_t rows, int K, int8_t* q, int ldq, float* scale,
+                             void* stream);
+
+/*
+ * hq_int8_matmul (R24): for every rank r, row t and feature n, with the sum in int32 (exact):
+ *   acc = sum_k a[r][t][k] * w[r][n][k]
+ *   v   = (float(acc) * a_scale[r][t]) * w_scale[r][n];  bias:  v = v + bias[r][n]
+ *         (fp32, round to nearest at every step)
+ *   out[r][t][n] = v as fp32 (HQ_OUT_F32), or rounded to bf16 nearest-even (HQ_OUT_BF16)
+ *   a        int8 [P][T][K], rows lda bytes apart (rank r's rows start at a + r*T*lda)
+ *   a_scale  float [P][T]
+ *   w        int8 [P][H][K], rows ldw bytes apart: a channel's weights lie together
+ *   w_scale  float [P][H]
+ *   bias     bf16 [P][H], or NULL
+ *   out      [P][T][H], rows ldo elements apart; elements between H and ldo are left as they are.
+ *            With HQ_OUT_BF16 and ldo = H it is the x of hq_calibrate and hq_quantize_pack.
+ *   1 <= P <= 64; T >= 0 (0 enqueues nothing); 8 <= H <= HQ_INT8_MAX_H with H % 8 == 0;
+ *   1 <= K <= HQ_INT8_MAX_K; lda, ldw >= K and multiples of 16; ldo >= H and a multiple of 8; a, w,
+ *   w_scale, bias and out 16-byte, a_scale 4-byte aligned.  What lies between K and lda or ldw is not
+ *   used.
+ */
+hq_status hq_int8_matmul(const int8_t* a, int lda, const float* a_scale, const int8_t* w, int ldw,
+                         const float* w_scale, const uint16_t* bias_or_null, int P, int T, int H, int K, void* out,
+                         int ldo, hq_out_dtype out_dtype, void* stream);
+
+/*
+ * hq_int8_matmul_pack: the wire of the partial sum that hq_int8_matmul (bf16, no bias) would write,
+ * bit for bit as hq_quantize_pack makes it, with no partial sum in memory.  The weights' rows are in
+ * the wire's order: row c < H - k of w and w_scale is feature rest_idx[c], row H - k + j is feature
+ * keep_idx[j] (laid out once, after hq_select_topk).  inv_scale and zero are in the features' own
+ * order, as hq_select_topk writes them.
+ *   a .. K, w_scale   as above; 8 <= H <= 32768
+ *   k, keep_idx .. zero, codes, side   as in hq_quantize_pack
+ */
+hq_status hq_int8_matmul_pack(const int8_t* a, int lda, const float* a_scale, const int8_t* w, int ldw,
+                              const float* w_scale, int P, int T, int H, int K, int k, const int32_t* keep_idx,
+                              const int32_t* rest_idx, const float* inv_scale, const uint8_t* zero, uint32_t* codes,
+                              uint16_t* side, void* stream);
+
+/*
+ * hq_residual_norm (R25): the end of a block, on the sum that hq_dequant_reduce writes.  For every
+ * row t, in fp32:
+ *   u   = norm_post(y[t])            HQ_NORM_NONE: y itself
+ *   r'  = alpha * res[t] + beta * (gate[t / gate_rows] * u)       gate NULL: 1
+ *   res_out[t] = r' in the residual's type
+ *   n   = norm_pre(res_out[t])       (of the stored, rounded value)
+ *   h[t] = n as bf16; q[t], q_scale[t] = hq_quantize_tokens of that bf16 row
+ * with  HQ_NORM_RMS:    norm(v) = v / sqrt(mean(v^2) + eps) * weight + bias
+ *       HQ_NORM_LAYER:  norm(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
+ *   y         [T][H], bf16 or fp32 (y_dtype)
+ *   res, res_out  [T][H], bf16 or fp32 (res_dtype); res_out may be res itself
+ *   post_w, post_b, pre_w, pre_b   float [H], each may be NULL (weight 1, bias 0)
+ *   gate      bf16 [ceil(T / gate_rows)][H] or NULL: gate_rows >= 1 consecutive rows share one row of
+ *             gate (T: one learned gate for all; 1: one a token)
+ *   h         bf16 [T][H] or NULL
+ *   q, q_scale    int8 [T][H] with rows ldq bytes apart (>= H, a multiple of 16; what lies between is
+ *             left as it is) and float [T], both or neither.  With pre == HQ_NORM_NONE h and q are NULL.
+ *   T >= 0 (0 enqueues nothing); 8 <= H <= 32768 with H % 8 == 0; eps >= 0, alpha and beta finite;
+ *   q_scale 4-byte, every other array 16-byte aligned.
+ */
+typedef enum { HQ_NORM_NONE = 0, HQ_NORM_RMS = 1, HQ_NORM_LAYER = 2 } hq_norm_kind;
+hq_status hq_residual_norm(const void* y, hq_out_dtype y_dtype, const void* res, void* res_out,
+                           hq_out_dtype res_dtype, int T, int H, hq_norm_kind post, const float* post_w,
+                           const float* post_b, const uint16_t* gate, int gate_rows, float alpha, float beta,
+                           hq_norm_kind pre, const float* pre_w, const float* pre_b, float eps, uint16_t* h, int8_t* q,
+                           int ldq, float* q_scale, void* stream);
+
 /* A static string naming a status. */
 const char* hq_status_string(hq_status s);
 

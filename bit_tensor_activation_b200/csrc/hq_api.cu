@@ -56,6 +56,7 @@ struct DeviceInfo {
   int sms = 0;
   int qt_blocks = 0;
   bool select_smem_set = false;
+  bool matmul_smem_set[3] = {};
   OccupancyCache dequant_tma[2][2];  // [fp32 out][bf16 shards]
   OccupancyCache dequant_cp[2][2];
   OccupancyCache fused[2];           // [fp32 out]
@@ -544,10 +545,46 @@ hq_status matmul_check(const int8_t* a, int lda, const float* a_scale, const int
   return HQ_OK;
 }
 
+// [ranks][rows][cols] of `elem`-byte elements, rows `pitch` bytes apart and the ranks' rows back to
+// back, in boxes of box_rows x 128 bytes with the 128-byte swizzle.
+bool encode_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uint64_t elem, uint64_t cols, uint64_t rows,
+               uint64_t ranks, uint64_t pitch, uint32_t box_rows) {
+  if (!get_encode()) return false;
+  cuuint64_t dims[3] = {cols, rows, ranks};
+  cuuint64_t strides[2] = {pitch, pitch * rows};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / elem), box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kOut>
 hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
-  const dim3 grid((unsigned)ceil_div(p.H, hq::kMmSimpleTile), (unsigned)ceil_div(p.T, hq::kMmSimpleTile), (unsigned)p.P);
-  hq::int8_matmul_simple_kernel<kOut><<<grid, 256, 0, st>>>(p);
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != HQ_OK) return HQ_ERR_CUDA;
+  CUtensorMap map_a, map_w, map_out;
+  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, hq::kMmHalf) ||
+      !encode_3d(&map_w, p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.H, p.P, p.ldw, hq::kMmHalf))
+    return HQ_ERR_CUDA;
+  memset(&map_out, 0, sizeof map_out);
+  if (kOut == hq::kMmBf16 && !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.T, p.P, 2ull * p.ldo, 32))
+    return HQ_ERR_CUDA;
+  if (kOut == hq::kMmF32 && !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.H, p.T, p.P, 4ull * p.ldo, 32))
+    return HQ_ERR_CUDA;
+  auto kern = hq::int8_matmul_pair_kernel<kOut>;
+  const size_t smem = sizeof(hq::MmSmem) + 1024;
+  {
+    std::lock_guard<std::mutex> lock(g_dev_mu);
+    if (!d->matmul_smem_set[kOut]) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return HQ_ERR_CUDA;
+      d->matmul_smem_set[kOut] = true;
+    }
+  }
+  const long long tiles = (long long)p.P * ceil_div(p.T, hq::kMmTile) * ceil_div(p.H, hq::kMmTile);
+  const long long clusters = std::min<long long>(tiles, d->sms / 2);
+  kern<<<(unsigned)(2 * clusters), hq::kMmThreads, smem, st>>>(map_a, map_w, map_out, p, wait_limits());
   return launched();
 }
 

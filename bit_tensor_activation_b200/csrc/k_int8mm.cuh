@@ -6,7 +6,7 @@
 //   v   = (float(acc) * a_scale[r][t]) * w_scale[r][n] (+ bias[r][n]), one rounding a step
 #pragma once
 
-#include "hq_common.cuh"
+#include "hq_tc.cuh"
 
 namespace hq {
 
@@ -52,69 +52,273 @@ __device__ __forceinline__ float mm_value(int acc, float sa, float sw) {
   return __fmul_rn(__fmul_rn(__int2float_rn(acc), sa), sw);
 }
 
-constexpr int kMmSimpleTile = 64, kMmSimpleK = 64;
+// ------------------------------------------------------------------------------------------------
+// Many tokens: a pair of CTAs to a tile of 256 tokens x 256 features.
+//
+// tcgen05.mma with cta_group::2 takes M = 256, N = 256: each CTA of the pair loads its own 128 tokens
+// and its own 128 features (32 KB a step of K = 128 bytes) and holds the accumulators of its 128
+// tokens x 256 features, so an operand byte is read from L2 once for 256 rows of the other operand.
+// A 256 x 256 tile of int32 is half of tensor memory: two tiles take turns, and the epilogue of one
+// runs under the products of the next.  One cluster a pair of SMs walks the tiles, rank by rank.
+//
+// Warps 0-7 are the epilogue (warp w: lanes of tensor memory 32 (w % 4) .., columns 128 (w / 4) ..),
+// warp 8 loads, warp 9 of the first CTA issues the products.  Every wait is bounded (hq_tma.cuh).
+constexpr int kMmTile = 256;                                   // tokens and features of a pair's tile
+constexpr int kMmHalf = 128;                                   // of one CTA
+constexpr int kMmK = 128;                                      // bytes of K a step
+constexpr int kMmStages = 5;
+constexpr int kMmEpiWarps = 8;
+constexpr int kMmThreads = 32 * (kMmEpiWarps + 2);
+constexpr unsigned kMmStageBytes = 2 * kMmHalf * kMmK;         // one CTA's part of a step
+constexpr int kMmGroupM = 8;                                   // token tiles that share a sweep over the features
 
-__device__ __forceinline__ uint32_t mm_load4(const int8_t* __restrict__ row, int k, int K) {
-  if (k + 4 <= K) return *reinterpret_cast<const uint32_t*>(row + k);
-  uint32_t w = 0;
-  for (int i = 0; k + i < K; ++i) w |= (uint32_t)(uint8_t)row[k + i] << (8 * i);
-  return w;
+struct MmSmem {
+  alignas(1024) unsigned char a[kMmStages][kMmHalf * kMmK];
+  alignas(1024) unsigned char b[kMmStages][kMmHalf * kMmK];
+  alignas(1024) unsigned char out[kMmEpiWarps][32 * 128];      // a warp's 32 rows of 128 bytes on their way out
+  float col[2][2][kMmTile];                                    // [tile parity][w_scale; bias or inv_scale]
+  int lo[2][kMmTile];
+  uint64_t full[kMmStages], empty[kMmStages], acc_full[2], acc_empty[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+static_assert(sizeof(MmSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
+
+// Tile i of the walk: rank, token tile, feature tile.  Within a rank, groups of kMmGroupM token tiles
+// sweep all features, so that a wave of tiles shares its operands in L2.
+struct MmTileAt {
+  int r, t0, n0;
+};
+__device__ __forceinline__ MmTileAt mm_tile(int i, int mt, int nt) {
+  const int r = i / (mt * nt);
+  int j = i - r * mt * nt;
+  const int g = j / (kMmGroupM * nt);
+  const int rows = min(kMmGroupM, mt - g * kMmGroupM);
+  j -= g * kMmGroupM * nt;
+  const int n = j / rows;
+  return MmTileAt{r, (g * kMmGroupM + j - n * rows) * kMmTile, n * kMmTile};
+}
+
+// Eight bf16 values (w: four words) of one token as one word of codes.
+__device__ __forceinline__ uint32_t wire_word(const uint32_t* w, const float* inv, const int* lo) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const WireCol c{inv[j], lo[j]};
+    word |= wire_code((j & 1) ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]), c) << (4 * j);
+  }
+  return word;
 }
 
 template <int kOut>
-__global__ void __launch_bounds__(256) int8_matmul_simple_kernel(const MmArgs p) {
-  __shared__ uint32_t sa[kMmSimpleTile][kMmSimpleK / 4 + 1], sb[kMmSimpleTile][kMmSimpleK / 4 + 1];
-  const int n0 = blockIdx.x * kMmSimpleTile, t0 = blockIdx.y * kMmSimpleTile, r = blockIdx.z;
-  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;  // 8 x 32: 8 columns and 2 rows a thread
-  int acc[2][8] = {};
-  for (int k0 = 0; k0 < p.K; k0 += kMmSimpleK) {
-    for (int i = threadIdx.x; i < kMmSimpleTile * kMmSimpleK / 4; i += 256) {
-      const int row = i / (kMmSimpleK / 4), c = i % (kMmSimpleK / 4), k = k0 + 4 * c;
-      sa[row][c] = t0 + row < p.T && k < p.K ? mm_load4(p.a + ((size_t)r * p.T + t0 + row) * p.lda, k, p.K) : 0u;
-      sb[row][c] = n0 + row < p.H && k < p.K ? mm_load4(p.w + ((size_t)r * p.H + n0 + row) * p.ldw, k, p.K) : 0u;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
+    int8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                            const __grid_constant__ CUtensorMap map_out, const MmArgs p, WaitLimits lim) {
+  extern __shared__ unsigned char s_raw[];
+  MmSmem& sm = *reinterpret_cast<MmSmem*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t cta = cluster_ctarank();
+  const int mt = (p.T + kMmTile - 1) / kMmTile, nt = (p.H + kMmTile - 1) / kMmTile;
+  const int tiles = p.P * mt * nt, step = gridDim.x / 2, first = blockIdx.x / 2;
+  const int kc = (p.K + kMmK - 1) / kMmK;
+  volatile int* abort = &sm.abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMmStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
     }
-    __syncthreads();
-    for (int c = 0; c < kMmSimpleK / 4; ++c)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          acc[i][j] = __dp4a((int)sa[ty * 2 + i][c], (int)sb[tx * 8 + j][c], acc[i][j]);
-    __syncthreads();
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], 2 * kMmEpiWarps);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_barrier_init();
   }
-  const int n = n0 + tx * 8;
-  if (n >= p.H) return;
-  for (int i = 0; i < 2; ++i) {
-    const int t = t0 + ty * 2 + i;
-    if (t >= p.T) return;
-    const size_t row = (size_t)r * p.T + t;
-    const float s = __ldg(p.a_scale + row);
-    float v[8];
-    for (int j = 0; j < 8; ++j) {
-      v[j] = mm_value(acc[i][j], s, __ldg(p.w_scale + (size_t)r * p.H + n + j));
-      if (kOut != kMmWire && p.bias) v[j] = __fadd_rn(v[j], bf16_lo(__ldg(p.bias + (size_t)r * p.H + n + j)));
+  if (warp == kMmEpiWarps + 1) tc_alloc<2>(&sm.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp == kMmEpiWarps) {  // ---------------------------------------------- loads
+    if (lane == 0) {
+      prefetch_tensor_map(&map_a);
+      prefetch_tensor_map(&map_w);
+      producer_start_delay(lim.start_delay);
+      int i = 0;
+      bool go = true;
+      for (int t = first; t < tiles && go; t += step) {
+        const MmTileAt at = mm_tile(t, mt, nt);
+        for (int c = 0; c < kc; ++c, ++i) {
+          const int s = i % kMmStages;
+          if (i >= kMmStages && !mbar_wait(&sm.empty[s], ((i / kMmStages) - 1) & 1, abort, lim.producer)) {
+            go = false;
+            break;
+          }
+          if (cta == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kMmStageBytes);
+          const uint32_t bar = cluster_addr(smem_addr(&sm.full[s]), 0);
+          tma_load_3d_pair(smem_addr(sm.a[s]), &map_a, c * kMmK, at.t0 + (int)cta * kMmHalf, at.r, bar);
+          tma_load_3d_pair(smem_addr(sm.b[s]), &map_w, c * kMmK, at.n0 + (int)cta * kMmHalf, at.r, bar);
+        }
+      }
+      // after an abort: the pair's loads have landed before either CTA leaves (the first CTA counts both)
+      if (*abort && cta == 0) {
+        int ignore = 0;
+        for (int j = max(0, i - kMmStages); j < i; ++j)
+          mbar_wait(&sm.full[j % kMmStages], (j / kMmStages) & 1, &ignore, lim.producer);
+      }
     }
-    if (kOut == kMmF32) {
-      for (int j = 0; j < 8; ++j) static_cast<float*>(p.out)[row * p.ldo + n + j] = v[j];
-      continue;
+  } else if (warp == kMmEpiWarps + 1) {  // ---------------------------------- products
+    if (cta == 0 && lane == 0) {
+      constexpr uint32_t idesc = tc_idesc(kMmTile, kMmTile);
+      int i = 0, n = 0;
+      bool go = true;
+      for (int t = first; t < tiles && go; t += step, ++n) {
+        const int b = n & 1;
+        if (n >= 2 && !mbar_wait(&sm.acc_empty[b], ((n >> 1) - 1) & 1, abort, lim.producer)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + b * kMmTile;
+        for (int c = 0; c < kc; ++c, ++i) {
+          const int s = i % kMmStages;
+          if (!mbar_wait(&sm.full[s], (i / kMmStages) & 1, abort, lim.consumer)) {
+            go = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = tc_desc(smem_addr(sm.a[s])), db = tc_desc(smem_addr(sm.b[s]));
+#pragma unroll
+          for (int k = 0; k < kMmK / 32; ++k) tc_mma<2>(d, da + 2 * k, db + 2 * k, idesc, c > 0 || k > 0);
+          tc_commit<2>(&sm.empty[s]);
+        }
+        if (go) tc_commit<2>(&sm.acc_full[b]);
+      }
+      if (*abort) {  // the products in flight are done before tensor memory is freed
+        int ignore = 0;
+        tc_commit<2>(&sm.drain);
+        mbar_wait(&sm.drain, 0, &ignore, lim.producer);
+      }
     }
-    uint32_t b[4];
-    for (int j = 0; j < 4; ++j) b[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-    if (kOut == kMmBf16) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.ldo + n) = make_uint4(b[0], b[1], b[2], b[3]);
-      continue;
-    }
+  } else {  // ------------------------------------------------------------------ epilogue
+    const int quad = warp & 3, side = warp >> 2;  // lanes 32 quad .., columns 128 side ..
+    const int tid = threadIdx.x;
+    const uint32_t stage = smem_addr(sm.out[warp]);
     const int Hr = p.H - p.k;
-    if (n < Hr) {
-      uint32_t word = 0;
-      for (int j = 0; j < 8; ++j)
-        word |= wire_code((j & 1) ? bf16_hi(b[j / 2]) : bf16_lo(b[j / 2]), wire_col(p, r, n + j)) << (4 * j);
-      p.codes[row * (Hr / 8) + n / 8] = word;
-    } else {
-      for (int j = 0; j < 8; ++j)
-        p.side[((size_t)r * p.k + (n - Hr) + j) * p.T + t] = (uint16_t)(b[j / 2] >> (16 * (j & 1)));
+    int n = 0;
+    bool ok = true;  // of the whole warp; a warp that gave up stops all of them at the next barrier
+    for (int t = first; t < tiles; t += step, ++n) {
+      const int b = n & 1;
+      const MmTileAt at = mm_tile(t, mt, nt);
+      {  // the columns' parameters, fetched while the products run
+        const int c = at.n0 + tid;
+        const size_t g = (size_t)at.r * p.H + c;
+        sm.col[b][0][tid] = c < p.H ? __ldg(p.w_scale + g) : 0.0f;
+        if (kOut == kMmWire) {
+          WireCol w{0.0f, 0};
+          if (c < Hr) w = wire_col(p, at.r, c);
+          sm.col[b][1][tid] = w.inv;
+          sm.lo[b][tid] = w.lo;
+        } else {
+          sm.col[b][1][tid] = p.bias && c < p.H ? bf16_lo(__ldg(p.bias + g)) : 0.0f;
+        }
+      }
+      const int row = at.t0 + (int)cta * kMmHalf + 32 * quad;  // the warp's first token
+      const float sa = row + lane < p.T ? __ldg(p.a_scale + (size_t)at.r * p.T + row + lane) : 0.0f;
+      if (named_barrier_or(32 * kMmEpiWarps, !ok)) break;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.acc_full[b], (n >> 1) & 1, abort, lim.consumer));
+      if (!ok) continue;
+      tc_fence_after();
+      const uint32_t acc = tmem + b * kMmTile + ((uint32_t)(32 * quad) << 16) + kMmHalf * side;
+      const float* col = sm.col[b][0] + kMmHalf * side;
+      const float* col2 = sm.col[b][1] + kMmHalf * side;
+      const int* lo = sm.lo[b] + kMmHalf * side;
+#pragma unroll 1
+      for (int c = 0; c < kMmHalf; c += 32) {
+        uint32_t v[32];
+        tc_load32(acc + c, v);
+        tc_load_wait();
+        if (c + 32 == kMmHalf) {  // the tile's last read: its columns may be written again
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&sm.acc_empty[b]), 0));
+        }
+        const int n0 = at.n0 + kMmHalf * side + c;
+        if (n0 >= p.H || row >= p.T) continue;
+        float f[32];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(col + c + j);
+          fmul2(f[j], f[j + 1], __int2float_rn((int)v[j]), __int2float_rn((int)v[j + 1]), sa, sa);
+          fmul2(f[j + 2], f[j + 3], __int2float_rn((int)v[j + 2]), __int2float_rn((int)v[j + 3]), sa, sa);
+          fmul2(f[j], f[j + 1], f[j], f[j + 1], w.x, w.y);
+          fmul2(f[j + 2], f[j + 3], f[j + 2], f[j + 3], w.z, w.w);
+        }
+        if (kOut != kMmWire && p.bias) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(col2 + c + j);
+            fadd2(f[j], f[j + 1], f[j], f[j + 1], w.x, w.y);
+            fadd2(f[j + 2], f[j + 3], f[j + 2], f[j + 3], w.z, w.w);
+          }
+        }
+        // 16-byte piece q of row `lane` lies at piece q ^ (lane % 8): the store's 128-byte swizzle
+        if (kOut == kMmF32) {
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_shared16(stage + lane * 128 + ((q ^ (lane & 7)) << 4), __float_as_uint(f[4 * q]),
+                        __float_as_uint(f[4 * q + 1]), __float_as_uint(f[4 * q + 2]), __float_as_uint(f[4 * q + 3]));
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_3d(&map_out, stage, n0, row, at.r);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+          if (kOut == kMmBf16) {
+            const int half = (c >> 5) & 1;  // 64 columns to a store
+            if (half == 0) {
+              if (lane == 0) tma_store_wait_read();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              st_shared16(stage + lane * 128 + (((4 * half + q) ^ (lane & 7)) << 4), w[4 * q], w[4 * q + 1], w[4 * q + 2],
+                          w[4 * q + 3]);
+            if (half == 1 || n0 + 32 >= p.H) {
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) tma_store_3d(&map_out, stage, n0 - 32 * half, row, at.r);
+            }
+          } else if (row + lane < p.T) {
+            const size_t tok = (size_t)at.r * p.T + row + lane;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int nn = n0 + 8 * q;
+              if (nn < Hr) {
+                p.codes[tok * (Hr / 8) + nn / 8] = wire_word(w + 4 * q, col2 + c + 8 * q, lo + c + 8 * q);
+              } else if (nn < p.H) {
+                uint16_t* s = p.side + ((size_t)at.r * p.k + (nn - Hr)) * p.T + row + lane;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[(size_t)j * p.T] = (uint16_t)(w[4 * q + j / 2] >> (16 * (j & 1)));
+              }
+            }
+          }
+        }
+      }
     }
+    if (lane == 0) tma_store_wait_read();
   }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA's memory goes while the other still counts on it
+  tc_fence_after();
+  if (warp == kMmEpiWarps + 1) tc_dealloc<2>(tmem, 512);
 }
 
 }  // namespace hq

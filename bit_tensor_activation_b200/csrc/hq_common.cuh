@@ -257,14 +257,16 @@ __device__ __forceinline__ GroupLayout group_layout_list(const int* list, int n,
   return L;
 }
 
-// Column index read from keep_idx / rest_idx, clamped into [0, H) with the error recorded.
-__device__ __forceinline__ int checked_col(const int32_t* __restrict__ idx, int j, int H) {
-  int h = __ldg(idx + j);
+// A column index of keep_idx / rest_idx, clamped into [0, H) with the error recorded.
+__device__ __forceinline__ int checked_index(int h, int H) {
   if (h < 0 || h >= H) {
     record_error(HQ_ERR_BAD_INDEX);
     h = 0;
   }
   return h;
+}
+__device__ __forceinline__ int checked_col(const int32_t* __restrict__ idx, int j, int H) {
+  return checked_index(__ldg(idx + j), H);
 }
 
 }  // namespace hq

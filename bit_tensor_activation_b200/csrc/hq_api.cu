@@ -546,17 +546,17 @@ hq_status matmul_check(const int8_t* a, int lda, const float* a_scale, const int
 }
 
 // [ranks][rows][cols] of `elem`-byte elements, rows `pitch` bytes apart and the ranks' rows back to
-// back, in boxes of box_rows x 128 bytes with the 128-byte swizzle.
+// back, in boxes of box_rows x box_bytes (128 or 64) with the swizzle of that width.
 bool encode_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uint64_t elem, uint64_t cols, uint64_t rows,
-               uint64_t ranks, uint64_t pitch, uint32_t box_rows) {
+               uint64_t ranks, uint64_t pitch, uint32_t box_rows, uint32_t box_bytes) {
   if (!get_encode()) return false;
   cuuint64_t dims[3] = {cols, rows, ranks};
   cuuint64_t strides[2] = {pitch, pitch * rows};
-  cuuint32_t box[3] = {(cuuint32_t)(128 / elem), box_rows, 1};
+  cuuint32_t box[3] = {(cuuint32_t)(box_bytes / elem), box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return g_encode(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int kOut>
@@ -564,13 +564,13 @@ hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
   DeviceInfo* d = nullptr;
   if (device_info(&d) != HQ_OK) return HQ_ERR_CUDA;
   CUtensorMap map_a, map_w, map_out;
-  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, hq::kMmHalf) ||
-      !encode_3d(&map_w, p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.H, p.P, p.ldw, hq::kMmHalf))
+  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, hq::kMmHalf, 128) ||
+      !encode_3d(&map_w, p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.H, p.P, p.ldw, hq::kMmHalf, 128))
     return HQ_ERR_CUDA;
   memset(&map_out, 0, sizeof map_out);
-  if (kOut == hq::kMmBf16 && !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.T, p.P, 2ull * p.ldo, 32))
+  if (kOut == hq::kMmBf16 && !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.T, p.P, 2ull * p.ldo, 32, 64))
     return HQ_ERR_CUDA;
-  if (kOut == hq::kMmF32 && !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.H, p.T, p.P, 4ull * p.ldo, 32))
+  if (kOut == hq::kMmF32 && !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.H, p.T, p.P, 4ull * p.ldo, 32, 64))
     return HQ_ERR_CUDA;
   auto kern = hq::int8_matmul_pair_kernel<kOut>;
   const size_t smem = sizeof(hq::MmSmem) + 1024;

@@ -42,30 +42,35 @@ enum MmOut { kMmBf16 = 0, kMmF32 = 1, kMmWire = 2 };
 // A 256 x 256 tile of int32 is half of tensor memory: two tiles take turns, and the epilogue of one
 // runs under the products of the next.  One cluster a pair of SMs walks the tiles, rank by rank.
 //
-// Warps 0-7 are the epilogue (warp w: lanes of tensor memory 32 (w % 4) .., columns 128 (w / 4) ..),
-// warp 8 loads, warp 9 of the first CTA issues the products.  Every wait is bounded (hq_tma.cuh).
+// Warps 0-11 are the epilogue: three warps share the 32 lanes (tokens) of tensor memory that a warp can
+// read and take its chunks of 32 columns in turn, from one tile to the next.  Warp 12 loads, warp 13 of
+// the first CTA issues the products.  Every wait is bounded (hq_tma.cuh).
 constexpr int kMmTile = 256;                                   // tokens and features of a pair's tile
 constexpr int kMmHalf = 128;                                   // of one CTA
 constexpr int kMmK = 128;                                      // bytes of K a step
 constexpr int kMmStages = 5;
-constexpr int kMmEpiWarps = 8;
+constexpr int kMmEpiWarps = 12;
+constexpr int kMmSides = kMmEpiWarps / 4;                      // epilogue warps that share 32 lanes of tensor memory
+constexpr int kMmChunks = kMmTile / 32;                        // 32 columns at a time
+constexpr int kMmWarpChunks = (kMmChunks + kMmSides - 1) / kMmSides;
 constexpr int kMmThreads = 32 * (kMmEpiWarps + 2);
 constexpr unsigned kMmStageBytes = 2 * kMmHalf * kMmK;         // one CTA's part of a step
 constexpr int kMmGroupM = 8;                                   // token tiles that share a sweep over the features
 
-// The parameters of a warp's 128 columns.
+// The parameters of 32 columns.
 struct MmCols {
-  alignas(16) float scale[kMmHalf];
-  alignas(16) float second[kMmHalf];  // bias, or the wire's inv_scale
-  alignas(16) float lo[kMmHalf];      // -zero
-  uint32_t zeros[kMmHalf / 8];        // the zero points of 8 columns as one word of codes
+  alignas(16) float scale[32];
+  alignas(16) float second[32];  // bias, or the wire's inv_scale
+  alignas(16) float lo[32];      // -zero
+  alignas(16) float hi[32];      // 15 - zero
+  uint32_t zeros[4];             // the zero points of 8 columns as one word of codes
 };
 
 struct MmSmem {
   alignas(1024) unsigned char a[kMmStages][kMmHalf * kMmK];
   alignas(1024) unsigned char b[kMmStages][kMmHalf * kMmK];
-  alignas(1024) unsigned char out[kMmEpiWarps][32 * 128];      // a warp's 32 rows of 128 bytes on their way out
-  MmCols col[kMmEpiWarps];
+  alignas(1024) unsigned char out[kMmEpiWarps][32 * 64];       // a warp's 32 rows of 64 bytes on their way out
+  MmCols col[kMmEpiWarps][kMmWarpChunks];
   uint64_t full[kMmStages], empty[kMmStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort;
@@ -92,11 +97,21 @@ __device__ __forceinline__ MmTileAt mm_tile(int i, int mt, int nt) {
 // inv and lo.  clamp(rint(t) + zero, 0, 15) = zero + rint(clamp(t, -zero, 15 - zero)), the bounds being
 // integers; adding 1.5 * 2^23 rounds to an integer, half to even, and leaves it in the low bits.  A NaN
 // (code: the zero point) shows in the sum of the products, and that word is made one code at a time.
-__device__ __forceinline__ uint32_t wire_word(const uint32_t* w, const float* inv, const float* lo, uint32_t zeros) {
+__device__ __noinline__ uint32_t wire_word_slow(float4 ta, float4 tb, const float* lo) {
+  const float t[8] = {ta.x, ta.y, ta.z, ta.w, tb.x, tb.y, tb.z, tb.w};
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int l = (int)lo[j], c = __float2int_rn(t[j]);  // saturating; NaN -> 0
+    word |= (uint32_t)(min(max(c, l), l + 15) - l) << (4 * j);
+  }
+  return word;
+}
+__device__ __forceinline__ uint32_t wire_word(const uint32_t* w, const MmCols& cols, int c) {
   float t[8];
 #pragma unroll
   for (int j = 0; j < 8; j += 4) {
-    const float4 i4 = *reinterpret_cast<const float4*>(inv + j);
+    const float4 i4 = *reinterpret_cast<const float4*>(cols.second + c + j);
     fmul2(t[j], t[j + 1], bf16_lo(w[j / 2]), bf16_hi(w[j / 2]), i4.x, i4.y);
     fmul2(t[j + 2], t[j + 3], bf16_lo(w[j / 2 + 1]), bf16_hi(w[j / 2 + 1]), i4.z, i4.w);
   }
@@ -105,89 +120,80 @@ __device__ __forceinline__ uint32_t wire_word(const uint32_t* w, const float* in
   fadd2(s2, s3, t[4], t[5], t[6], t[7]);
   fadd2(s0, s1, s0, s1, s2, s3);
   s0 = __fadd_rn(s0, s1);
-  if (s0 != s0) {
-    uint32_t word = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int l = (int)lo[j], c = __float2int_rn(t[j]);  // saturating; NaN -> 0
-      word |= (uint32_t)(min(max(c, l), l + 15) - l) << (4 * j);
-    }
-    return word;
-  }
   constexpr uint32_t kOnes = 0x11111111u;
-  uint32_t word = zeros - 0x4B400000u * kOnes;  // the constant's share of the sum below, modulo 2^32
+  uint32_t word = cols.zeros[c / 8] - 0x4B400000u * kOnes;  // the constant's share of the sum below, modulo 2^32
 #pragma unroll
   for (int j = 0; j < 8; j += 4) {
-    const float4 l4 = *reinterpret_cast<const float4*>(lo + j);
-    const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      float a = fminf(fmaxf(t[j + i], l[i]), __fadd_rn(l[i], 15.0f));
-      float b = fminf(fmaxf(t[j + i + 1], l[i + 1]), __fadd_rn(l[i + 1], 15.0f));
-      fadd2(a, b, a, b, 12582912.0f, 12582912.0f);
-      word += (__float_as_uint(a) << (4 * (j + i))) + (__float_as_uint(b) << (4 * (j + i + 1)));
-    }
+    const float4 l = *reinterpret_cast<const float4*>(cols.lo + c + j);
+    const float4 h = *reinterpret_cast<const float4*>(cols.hi + c + j);
+    float a0, a1, a2, a3;
+    fadd2(a0, a1, fminf(fmaxf(t[j], l.x), h.x), fminf(fmaxf(t[j + 1], l.y), h.y), 12582912.0f, 12582912.0f);
+    fadd2(a2, a3, fminf(fmaxf(t[j + 2], l.z), h.z), fminf(fmaxf(t[j + 3], l.w), h.w), 12582912.0f, 12582912.0f);
+    word = (__float_as_uint(a0) << (4 * j)) + word;
+    word = (__float_as_uint(a1) << (4 * j + 4)) + word;
+    word = (__float_as_uint(a2) << (4 * j + 8)) + word;
+    word = (__float_as_uint(a3) << (4 * j + 12)) + word;
   }
+  if (s0 != s0)
+    word = wire_word_slow(make_float4(t[0], t[1], t[2], t[3]), make_float4(t[4], t[5], t[6], t[7]), cols.lo + c);
   return word;
 }
 
-// A lane's four columns' parameters on their way to shared memory: fetched a tile ahead.
+// A lane's column of each of its warp's chunks, fetched a tile ahead of its use: chunk j0 + kMmSides i
+// of the 32 columns each from feature n0.
 template <int kOut>
 struct MmFetch {
-  float4 scale, second;
-  int4 rest;
-  uint32_t zero;  // four bytes
+  float scale[kMmWarpChunks], second[kMmWarpChunks];
+  int rest[kMmWarpChunks];
+  uint32_t zero[kMmWarpChunks];
 
-  __device__ __forceinline__ void start(const MmArgs& p, int r, int c) {
-    scale = second = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    rest = make_int4(0, 0, 0, 0);
-    zero = 0;
-    if (c < p.H) {
+  __device__ __forceinline__ static int column(int n0, int j0, int i, int lane) { return n0 + 32 * (j0 + kMmSides * i) + lane; }
+
+  __device__ __forceinline__ void start(const MmArgs& p, int r, int n0, int j0, int lane) {
+#pragma unroll
+    for (int i = 0; i < kMmWarpChunks; ++i) {
+      const int c = column(n0, j0, i, lane);
       const size_t g = (size_t)r * p.H + c;
-      scale = __ldg(reinterpret_cast<const float4*>(p.w_scale + g));
-      if (kOut != kMmWire && p.bias) {
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + g));
-        second = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
-      }
+      const bool on = j0 + kMmSides * i < kMmChunks && c < p.H;
+      scale[i] = on ? __ldg(p.w_scale + g) : 0.0f;
+      second[i] = kOut != kMmWire && p.bias && on ? bf16_lo(__ldg(p.bias + g)) : 0.0f;
+      rest[i] = kOut == kMmWire && on && c < p.H - p.k ? __ldg(p.rest_idx + c) : 0;
+      zero[i] = 0;
     }
-    if (kOut == kMmWire && c < p.H - p.k)
-      rest = make_int4(__ldg(p.rest_idx + c), __ldg(p.rest_idx + c + 1), __ldg(p.rest_idx + c + 2),
-                       __ldg(p.rest_idx + c + 3));
   }
   // The wire's grids, once the features are known.
-  __device__ __forceinline__ void grids(const MmArgs& p, int r, int c) {
-    if (kOut != kMmWire || c >= p.H - p.k) return;
-    rest = make_int4(checked_index(rest.x, p.H), checked_index(rest.y, p.H), checked_index(rest.z, p.H),
-                     checked_index(rest.w, p.H));
-    const float* inv = p.inv_scale + (size_t)r * p.H;
-    const uint8_t* z = p.zero + (size_t)r * p.H;
-    second = make_float4(__ldg(inv + rest.x), __ldg(inv + rest.y), __ldg(inv + rest.z), __ldg(inv + rest.w));
-    zero = (uint32_t)__ldg(z + rest.x) | (uint32_t)__ldg(z + rest.y) << 8 | (uint32_t)__ldg(z + rest.z) << 16 |
-           (uint32_t)__ldg(z + rest.w) << 24;
+  __device__ __forceinline__ void grids(const MmArgs& p, int r, int n0, int j0, int lane) {
+#pragma unroll
+    for (int i = 0; i < kMmWarpChunks; ++i) {
+      if (j0 + kMmSides * i >= kMmChunks || column(n0, j0, i, lane) >= p.H - p.k) continue;
+      const size_t g = (size_t)r * p.H + checked_index(rest[i], p.H);
+      second[i] = __ldg(p.inv_scale + g);
+      zero[i] = __ldg(p.zero + g);
+    }
   }
-  __device__ __forceinline__ void store(MmCols& s, int lane) const {
-    *reinterpret_cast<float4*>(s.scale + 4 * lane) = scale;
-    *reinterpret_cast<float4*>(s.second + 4 * lane) = second;
-    if (kOut == kMmWire) {
-      const uint32_t z0 = zero & 0xFFu, z1 = (zero >> 8) & 0xFFu, z2 = (zero >> 16) & 0xFFu, z3 = zero >> 24;
-      *reinterpret_cast<float4*>(s.lo + 4 * lane) = make_float4(-(float)z0, -(float)z1, -(float)z2, -(float)z3);
-      uint32_t w = (z0 + (z1 << 4) + (z2 << 8) + (z3 << 12)) << (16 * (lane & 1));
-      w += __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-      if ((lane & 1) == 0) s.zeros[lane >> 1] = w;
+  __device__ __forceinline__ void store(MmCols* s, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kMmWarpChunks; ++i) {
+      s[i].scale[lane] = scale[i];
+      s[i].second[lane] = second[i];
+      if (kOut != kMmWire) continue;
+      s[i].lo[lane] = -(float)zero[i];
+      s[i].hi[lane] = 15.0f - (float)zero[i];
+      uint32_t w = zero[i] << (4 * (lane & 7));
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, off);
+      if ((lane & 7) == 0) s[i].zeros[lane >> 3] = w;
     }
   }
 };
 
-// `n` words of one token's codes, as widely as their address allows.
-__device__ __forceinline__ void store_words8(uint32_t* p, const uint32_t* w, int n, int align) {
-  if (n == 8 && align == 32) {
-    st_global32(p, w);
-  } else if (n == 8 && align == 16) {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+// `n` words of one token's codes.
+__device__ __forceinline__ void store_words(uint32_t* p, const uint32_t* w, int n, bool wide) {
+  if (n == 4 && wide) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
       if (i < n) p[i] = w[i];
   }
 }
@@ -284,64 +290,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       }
     }
   } else {  // ------------------------------------------------------------------ epilogue
-    const int quad = warp & 3, side = warp >> 2;  // lanes 32 quad .., columns 128 side ..
+    const int quad = warp & 3, side = warp >> 2;
     const uint32_t stage = smem_addr(sm.out[warp]);
-    MmCols& cols = sm.col[warp];
+    MmCols* const cols_of = sm.col[warp];
     const int Hr = p.H - p.k;
-    const int word_align = Hr % 64 == 0 && ((uintptr_t)p.codes & 31) == 0 ? 32 : Hr % 32 == 0 && ((uintptr_t)p.codes & 15) == 0 ? 16 : 4;
+    const bool wide = Hr % 32 == 0 && ((uintptr_t)p.codes & 15) == 0;  // a token's words of codes start on 16 bytes
     MmFetch<kOut> next;
     float next_sa = 0.0f;
-    auto fetch = [&](int t) {
-      if (t >= tiles) return;
-      const MmTileAt at = mm_tile(t, mt, nt);
+    // the warp's first chunk of its n-th tile: chunks 0, 1, .. of tile after tile go round the sides
+    auto first_chunk = [&](int n) { return (side + (kMmSides - kMmChunks % kMmSides) * n) % kMmSides; };
+    auto fetch = [&](const MmTileAt& at, int n) {
       const int row = at.t0 + (int)cta * kMmHalf + 32 * quad + lane;
       next_sa = row < p.T ? __ldg(p.a_scale + (size_t)at.r * p.T + row) : 0.0f;
-      next.start(p, at.r, at.n0 + kMmHalf * side + 4 * lane);
+      next.start(p, at.r, at.n0, first_chunk(n), lane);
     };
-    auto fetch_grids = [&](int t) {
-      if (kOut != kMmWire || t >= tiles) return;
-      const MmTileAt at = mm_tile(t, mt, nt);
-      next.grids(p, at.r, at.n0 + kMmHalf * side + 4 * lane);
-    };
-    fetch(first);
-    fetch_grids(first);
     int n = 0;
+    MmTileAt at = mm_tile(first, mt, nt);
+    fetch(at, 0);
+    if (kOut == kMmWire) next.grids(p, at.r, at.n0, first_chunk(0), lane);
     for (int t = first; t < tiles; t += step, ++n) {
       const int b = n & 1;
-      const MmTileAt at = mm_tile(t, mt, nt);
       const int row = at.t0 + (int)cta * kMmHalf + 32 * quad;  // the warp's first token
       const float sa = next_sa;
       __syncwarp();
-      next.store(cols, lane);
+      next.store(cols_of, lane);
       __syncwarp();
-      fetch(t + step);
+      const MmTileAt cur = at;
+      const bool more = t + step < tiles;
+      if (more) {
+        at = mm_tile(t + step, mt, nt);
+        fetch(at, n + 1);
+      }
       // every lane of the warp, or none
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.acc_full[b], (n >> 1) & 1, abort, lim.consumer))) break;
       tc_fence_after();
-      fetch_grids(t + step);
-      const uint32_t acc = tmem + b * kMmTile + ((uint32_t)(32 * quad) << 16) + kMmHalf * side;
-      const float* col = cols.scale;
-      const float* col2 = cols.second;
-      uint32_t words[8];
-      uint32_t ld[2][32];
-      tc_load32(acc, ld[0]);
-#pragma unroll
-      for (int c = 0; c < kMmHalf; c += 32) {
-        uint32_t(&v)[32] = ld[(c >> 5) & 1];
-        tc_load_wait(v);
-        if (c + 32 < kMmHalf) {  // the next columns come while these are worked on
-          tc_load32(acc + c + 32, ld[((c >> 5) + 1) & 1]);
-        } else {  // the tile's last read: its columns may be written again
+      if (kOut == kMmWire && more) next.grids(p, at.r, at.n0, first_chunk(n + 1), lane);
+      const uint32_t acc = tmem + b * kMmTile + ((uint32_t)(32 * quad) << 16);
+#pragma unroll 1
+      for (int j = first_chunk(n), i = 0; j < kMmChunks; j += kMmSides, ++i) {
+        const MmCols& cols = cols_of[i];
+        uint32_t v[32];
+        tc_load(acc + 32 * j, v);
+        if (j + kMmSides >= kMmChunks) {  // the warp's last read of the tile: its columns may be written again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&sm.acc_empty[b]), 0));
         }
-        const int n0 = at.n0 + kMmHalf * side + c;
+        const int n0 = cur.n0 + 32 * j;
         if (n0 >= p.H || row >= p.T) continue;
         float f[32];
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 w = *reinterpret_cast<const float4*>(col + c + j);
+          const float4 w = *reinterpret_cast<const float4*>(cols.scale + j);
           fmul2(f[j], f[j + 1], __int2float_rn((int)v[j]), __int2float_rn((int)v[j + 1]), sa, sa);
           fmul2(f[j + 2], f[j + 3], __int2float_rn((int)v[j + 2]), __int2float_rn((int)v[j + 3]), sa, sa);
           fmul2(f[j], f[j + 1], f[j], f[j + 1], w.x, w.y);
@@ -350,66 +350,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         if (kOut != kMmWire && p.bias) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(col2 + c + j);
+            const float4 w = *reinterpret_cast<const float4*>(cols.second + j);
             fadd2(f[j], f[j + 1], f[j], f[j + 1], w.x, w.y);
             fadd2(f[j + 2], f[j + 3], f[j + 2], f[j + 3], w.z, w.w);
           }
         }
-        // 16-byte piece q of row `lane` lies at piece q ^ (lane % 8): the store's 128-byte swizzle
-        if (kOut == kMmF32) {
+        // a store's 32 rows of 64 bytes: 16-byte piece q of row `lane` lies at piece q ^ (lane / 2 % 4)
+        auto send = [&](int at_col, const uint32_t* x) {
           if (lane == 0) tma_store_wait_read<0>();
           __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            st_shared16(stage + lane * 128 + ((q ^ (lane & 7)) << 4), __float_as_uint(f[4 * q]),
-                        __float_as_uint(f[4 * q + 1]), __float_as_uint(f[4 * q + 2]), __float_as_uint(f[4 * q + 3]));
+          for (int q = 0; q < 4; ++q)
+            st_shared16(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) tma_store_3d(&map_out, stage, n0, row, at.r);
-        } else {
-          uint32_t w[16];
+          if (lane == 0) tma_store_3d(&map_out, stage, at_col, row, cur.r);
+        };
+        if (kOut == kMmF32) {
+          uint32_t x[32];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            w[j] = kOut == kMmBf16 ? pack_bf16x2(f[2 * j], f[2 * j + 1]) : round_bf16x2(f[2 * j], f[2 * j + 1]);
-          if (kOut == kMmBf16) {
-            const int half = (c >> 5) & 1;  // 64 columns to a store
-            if (half == 0) {
-              if (lane == 0) tma_store_wait_read<0>();
-              __syncwarp();
-            }
+          for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(f[j]);
+          send(n0, x);
+          if (n0 + 16 < p.H) send(n0 + 16, x + 16);
+          continue;
+        }
+        uint32_t w[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              st_shared16(stage + lane * 128 + (((4 * half + q) ^ (lane & 7)) << 4), w[4 * q], w[4 * q + 1], w[4 * q + 2],
-                          w[4 * q + 3]);
-            if (half == 1 || n0 + 32 >= p.H) {
-              fence_async_smem();
-              __syncwarp();
-              if (lane == 0) tma_store_3d(&map_out, stage, n0 - 32 * half, row, at.r);
-            }
-          } else {
-            const int half = (c >> 5) & 1;  // 64 columns are 8 words
-            const size_t tok = (size_t)at.r * p.T + row + lane;
-            const bool live = row + lane < p.T;
+        for (int j = 0; j < 16; ++j)
+          w[j] = kOut == kMmBf16 ? pack_bf16x2(f[2 * j], f[2 * j + 1]) : round_bf16x2(f[2 * j], f[2 * j + 1]);
+        if (kOut == kMmBf16) {
+          send(n0, w);
+          continue;
+        }
+        const bool live = row + lane < p.T;
+        if (n0 < Hr) {
+          uint32_t words[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              words[4 * half + q] = wire_word(w + 4 * q, col2 + c + 8 * q, cols.lo + c + 8 * q, cols.zeros[c / 8 + q]);
-            const int first_col = n0 - 32 * half;
-            if (live && first_col < Hr && (half == 1 || n0 + 32 >= Hr))
-              store_words8(p.codes + tok * (Hr / 8) + first_col / 8, words, min(8, (Hr - first_col) / 8), word_align);
-            if (live && n0 + 32 > Hr) {  // kept features, 32 tokens of one beside one another
+          for (int q = 0; q < 4; ++q) words[q] = wire_word(w + 4 * q, cols, 8 * q);
+          if (live) store_words(p.codes + ((size_t)cur.r * p.T + row + lane) * (Hr / 8) + n0 / 8, words, min(4, (Hr - n0) / 8), wide);
+        }
+        if (live && n0 + 32 > Hr) {  // kept features: 32 tokens of one lie beside one another
+          uint16_t* s = p.side + ((long long)cur.r * p.k + (n0 - Hr)) * p.T + row + lane;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const int f0 = n0 + j - Hr;
-                const uint32_t x = (w[j / 2] >> (16 * (j & 1))) & 0xFFFFu;
-                if (f0 >= 0 && n0 + j < p.H)
-                  p.side[((size_t)at.r * p.k + f0) * p.T + row + lane] = (uint16_t)((x & 0x7FFFu) > 0x7F80u ? 0x7FC0u : x);
-              }
-            }
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t x = (w[j / 2] >> (16 * (j & 1))) & 0xFFFFu;
+            if (n0 + j >= Hr && n0 + j < p.H) s[(long long)j * p.T] = (uint16_t)((x & 0x7FFFu) > 0x7F80u ? 0x7FC0u : x);
           }
         }
       }
     }
-    if (lane == 0) tma_store_wait_read<0>();
+    if (kOut != kMmWire && lane == 0) tma_store_wait_read<0>();
   }
   __syncwarp();
   tc_fence_before();

@@ -61,9 +61,7 @@ constexpr int kMmGroupM = 8;                                   // token tiles th
 struct MmCols {
   alignas(16) float scale[32];
   alignas(16) float second[32];  // bias, or the wire's inv_scale
-  alignas(16) float lo[32];      // -zero
-  alignas(16) float hi[32];      // 15 - zero
-  uint32_t zeros[4];             // the zero points of 8 columns as one word of codes
+  alignas(16) int zero[32];      // the wire's zero point - kMagicBits
 };
 
 struct MmSmem {
@@ -78,64 +76,80 @@ struct MmSmem {
 
 static_assert(sizeof(MmSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
-// Tile i of the walk: rank, token tile, feature tile.  Within a rank, groups of kMmGroupM token tiles
-// sweep all features, so that a wave of tiles shares its operands in L2.
+// The walk over the tiles, rank by rank.  Within a rank, groups of kMmGroupM token tiles sweep all
+// features, so that a wave of tiles shares its operands in L2.  Quotients come from fp32 reciprocals and
+// one correction: they are below 2^20 (2^31 tokens are 2^20 groups), so the estimate is off by at most one.
 struct MmTileAt {
   int r, t0, n0;
 };
-__device__ __forceinline__ MmTileAt mm_tile(int i, int mt, int nt) {
-  const int r = i / (mt * nt);
-  int j = i - r * mt * nt;
-  const int g = j / (kMmGroupM * nt);
-  const int rows = min(kMmGroupM, mt - g * kMmGroupM);
-  j -= g * kMmGroupM * nt;
-  const int n = j / rows;
-  return MmTileAt{r, (g * kMmGroupM + j - n * rows) * kMmTile, n * kMmTile};
-}
+struct MmWalk {
+  int mt, nt, per_rank, r, j;
+  float inv_group;
 
-// Eight bf16 values (w: four words) of one token as one word of codes, the columns' parameters at
-// inv and lo.  clamp(rint(t) + zero, 0, 15) = zero + rint(clamp(t, -zero, 15 - zero)), the bounds being
-// integers; adding 1.5 * 2^23 rounds to an integer, half to even, and leaves it in the low bits.  A NaN
-// (code: the zero point) shows in the sum of the products, and that word is made one code at a time.
-__device__ __noinline__ uint32_t wire_word_slow(float4 ta, float4 tb, const float* lo) {
+  __device__ __forceinline__ MmWalk(const MmArgs& p, int i) {
+    mt = (p.T + kMmTile - 1) / kMmTile;
+    nt = (p.H + kMmTile - 1) / kMmTile;
+    per_rank = mt * nt;
+    r = i / per_rank;
+    j = i - r * per_rank;
+    inv_group = __frcp_rn((float)(kMmGroupM * nt));
+  }
+  __device__ __forceinline__ void advance(int step) {
+    for (j += step; j >= per_rank; j -= per_rank) ++r;
+  }
+  __device__ __forceinline__ MmTileAt at() const {
+    int g = __float2int_rz(__fmul_rn((float)j, inv_group));
+    int rem = j - g * kMmGroupM * nt;
+    if (rem < 0) --g, rem += kMmGroupM * nt;
+    if (rem >= kMmGroupM * nt) ++g, rem -= kMmGroupM * nt;
+    const int rows = min(kMmGroupM, mt - g * kMmGroupM);
+    const int n = rows == kMmGroupM ? rem / kMmGroupM : rem / rows;
+    return MmTileAt{r, (g * kMmGroupM + rem - n * rows) * kMmTile, n * kMmTile};
+  }
+};
+
+// Eight bf16 values (w: four words) of one token as one word of codes: clamp(rint(x * inv) + zero, 0, 15).
+// Adding 1.5 * 2^23 rounds a product below 2^22 to an integer, half to even, in the low bits of the sum;
+// with the zero point less the constant's bits that is rint + zero, which cvt.pack saturates to 0 .. 15
+// and puts beside the others.  Eight products with a larger one or a NaN among them are taken one by one
+// (their largest magnitude costs half an instruction each; clamping every one of them would cost two).
+constexpr int kMagicBits = 0x4B400000;  // 12582912.0f
+__device__ __noinline__ uint32_t wire_word_slow(float4 ta, float4 tb, const int* zero) {
   const float t[8] = {ta.x, ta.y, ta.z, ta.w, tb.x, tb.y, tb.z, tb.w};
   uint32_t word = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int l = (int)lo[j], c = __float2int_rn(t[j]);  // saturating; NaN -> 0
-    word |= (uint32_t)(min(max(c, l), l + 15) - l) << (4 * j);
+    const int z = zero[j] + kMagicBits, c = __float2int_rn(t[j]);  // saturating; NaN -> 0
+    word |= (uint32_t)(min(max(c, -z), 15 - z) + z) << (4 * j);
   }
   return word;
 }
 __device__ __forceinline__ uint32_t wire_word(const uint32_t* w, const MmCols& cols, int c) {
   float t[8];
+  int q[8];
 #pragma unroll
   for (int j = 0; j < 8; j += 4) {
-    const float4 i4 = *reinterpret_cast<const float4*>(cols.second + c + j);
-    fmul2(t[j], t[j + 1], bf16_lo(w[j / 2]), bf16_hi(w[j / 2]), i4.x, i4.y);
-    fmul2(t[j + 2], t[j + 3], bf16_lo(w[j / 2 + 1]), bf16_hi(w[j / 2 + 1]), i4.z, i4.w);
-  }
-  float s0, s1, s2, s3;
-  fadd2(s0, s1, t[0], t[1], t[2], t[3]);
-  fadd2(s2, s3, t[4], t[5], t[6], t[7]);
-  fadd2(s0, s1, s0, s1, s2, s3);
-  s0 = __fadd_rn(s0, s1);
-  constexpr uint32_t kOnes = 0x11111111u;
-  uint32_t word = cols.zeros[c / 8] - 0x4B400000u * kOnes;  // the constant's share of the sum below, modulo 2^32
-#pragma unroll
-  for (int j = 0; j < 8; j += 4) {
-    const float4 l = *reinterpret_cast<const float4*>(cols.lo + c + j);
-    const float4 h = *reinterpret_cast<const float4*>(cols.hi + c + j);
+    const float4 i = *reinterpret_cast<const float4*>(cols.second + c + j);
+    fmul2(t[j], t[j + 1], bf16_lo(w[j / 2]), bf16_hi(w[j / 2]), i.x, i.y);
+    fmul2(t[j + 2], t[j + 3], bf16_lo(w[j / 2 + 1]), bf16_hi(w[j / 2 + 1]), i.z, i.w);
+    const int4 z = *reinterpret_cast<const int4*>(cols.zero + c + j);
     float a0, a1, a2, a3;
-    fadd2(a0, a1, fminf(fmaxf(t[j], l.x), h.x), fminf(fmaxf(t[j + 1], l.y), h.y), 12582912.0f, 12582912.0f);
-    fadd2(a2, a3, fminf(fmaxf(t[j + 2], l.z), h.z), fminf(fmaxf(t[j + 3], l.w), h.w), 12582912.0f, 12582912.0f);
-    word = (__float_as_uint(a0) << (4 * j)) + word;
-    word = (__float_as_uint(a1) << (4 * j + 4)) + word;
-    word = (__float_as_uint(a2) << (4 * j + 8)) + word;
-    word = (__float_as_uint(a3) << (4 * j + 12)) + word;
+    fadd2(a0, a1, t[j], t[j + 1], 12582912.0f, 12582912.0f);
+    fadd2(a2, a3, t[j + 2], t[j + 3], 12582912.0f, 12582912.0f);
+    q[j] = __float_as_int(a0) + z.x, q[j + 1] = __float_as_int(a1) + z.y;
+    q[j + 2] = __float_as_int(a2) + z.z, q[j + 3] = __float_as_int(a3) + z.w;
   }
-  if (s0 != s0)
-    word = wire_word_slow(make_float4(t[0], t[1], t[2], t[3]), make_float4(t[4], t[5], t[6], t[7]), cols.lo + c);
+  float top;  // the largest |t|, or NaN
+  asm("{.reg .f32 a, b;\n\tmax.NaN.abs.f32 a, %1, %2, %3;\n\tmax.NaN.abs.f32 b, %4, %5, %6;\n\t"
+      "max.NaN.abs.f32 a, a, %7, %8;\n\tmax.NaN.abs.f32 %0, a, b, b;}"
+      : "=f"(top)
+      : "f"(t[0]), "f"(t[1]), "f"(t[2]), "f"(t[3]), "f"(t[4]), "f"(t[5]), "f"(t[6]), "f"(t[7]));
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 6; j >= 0; j -= 2)
+    asm("cvt.pack.sat.u4.s32.b32 %0, %1, %2, %0;" : "+r"(word) : "r"(q[j + 1]), "r"(q[j]));
+  if (!(top < 2097152.0f))
+    word = wire_word_slow(make_float4(t[0], t[1], t[2], t[3]), make_float4(t[4], t[5], t[6], t[7]), cols.zero + c);
   return word;
 }
 
@@ -176,13 +190,7 @@ struct MmFetch {
     for (int i = 0; i < kMmWarpChunks; ++i) {
       s[i].scale[lane] = scale[i];
       s[i].second[lane] = second[i];
-      if (kOut != kMmWire) continue;
-      s[i].lo[lane] = -(float)zero[i];
-      s[i].hi[lane] = 15.0f - (float)zero[i];
-      uint32_t w = zero[i] << (4 * (lane & 7));
-#pragma unroll
-      for (int off = 1; off < 8; off <<= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, off);
-      if ((lane & 7) == 0) s[i].zeros[lane >> 3] = w;
+      if (kOut == kMmWire) s[i].zero[lane] = (int)zero[i] - kMagicBits;
     }
   }
 };
@@ -206,8 +214,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   MmSmem& sm = *reinterpret_cast<MmSmem*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cta = cluster_ctarank();
-  const int mt = (p.T + kMmTile - 1) / kMmTile, nt = (p.H + kMmTile - 1) / kMmTile;
-  const int tiles = p.P * mt * nt, step = gridDim.x / 2, first = blockIdx.x / 2;
+  const int step = gridDim.x / 2, first = blockIdx.x / 2;
+  MmWalk walk(p, first);
+  const int tiles = p.P * walk.per_rank;
   const int kc = (p.K + kMmK - 1) / kMmK;
   volatile int* abort = &sm.abort;
 
@@ -238,8 +247,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       producer_start_delay(lim.start_delay);
       int i = 0;
       bool go = true;
-      for (int t = first; t < tiles && go; t += step) {
-        const MmTileAt at = mm_tile(t, mt, nt);
+      for (int t = first; t < tiles && go; t += step, walk.advance(step)) {
+        const MmTileAt at = walk.at();
         for (int c = 0; c < kc; ++c, ++i) {
           const int s = i % kMmStages;
           if (i >= kMmStages && !mbar_wait(&sm.empty[s], ((i / kMmStages) - 1) & 1, abort, lim.producer)) {
@@ -305,7 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       next.start(p, at.r, at.n0, first_chunk(n), lane);
     };
     int n = 0;
-    MmTileAt at = mm_tile(first, mt, nt);
+    MmTileAt at = walk.at();
     fetch(at, 0);
     if (kOut == kMmWire) next.grids(p, at.r, at.n0, first_chunk(0), lane);
     for (int t = first; t < tiles; t += step, ++n) {
@@ -318,13 +327,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       const MmTileAt cur = at;
       const bool more = t + step < tiles;
       if (more) {
-        at = mm_tile(t + step, mt, nt);
+        walk.advance(step);
+        at = walk.at();
         fetch(at, n + 1);
       }
       // every lane of the warp, or none
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.acc_full[b], (n >> 1) & 1, abort, lim.consumer))) break;
       tc_fence_after();
-      if (kOut == kMmWire && more) next.grids(p, at.r, at.n0, first_chunk(n + 1), lane);
       const uint32_t acc = tmem + b * kMmTile + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
       for (int j = first_chunk(n), i = 0; j < kMmChunks; j += kMmSides, ++i) {
@@ -336,6 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&sm.acc_empty[b]), 0));
         }
+        if (kOut == kMmWire && i == 1 && more) next.grids(p, at.r, at.n0, first_chunk(n + 1), lane);
         const int n0 = cur.n0 + 32 * j;
         if (n0 >= p.H || row >= p.T) continue;
         float f[32];

@@ -56,7 +56,8 @@ struct DeviceInfo {
   int sms = 0;
   int qt_blocks = 0;
   bool select_smem_set = false;
-  bool matmul_smem_set[3] = {};
+  bool pair_smem_set[3] = {};        // [output]
+  bool few_smem_set[3][4] = {};      // [output][tokens 16, 32, 64, 128]
   OccupancyCache dequant_tma[2][2];  // [fp32 out][bf16 shards]
   OccupancyCache dequant_cp[2][2];
   OccupancyCache fused[2];           // [fp32 out]
@@ -559,29 +560,75 @@ bool encode_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uin
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The dynamic shared memory of a kernel is raised to `bytes` once per device.
+template <typename Kernel>
+hq_status raise_smem(bool& done, Kernel kern, size_t bytes) {
+  std::lock_guard<std::mutex> lock(g_dev_mu);
+  if (!done && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+    return HQ_ERR_CUDA;
+  done = true;
+  return HQ_OK;
+}
+
+constexpr size_t kSmemPerSm = 227 * 1024;
+
+template <int kOut, int kTokens>
+hq_status launch_few(const hq::MmArgs& p, const CUtensorMap& map_w, DeviceInfo& d, cudaStream_t st) {
+  CUtensorMap map_a;
+  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, kTokens, 128)) return HQ_ERR_CUDA;
+  auto kern = hq::int8_matmul_few_kernel<kOut, kTokens>;
+  constexpr int kIdx = kTokens == 16 ? 0 : kTokens == 32 ? 1 : kTokens == 64 ? 2 : 3;
+  if (raise_smem(d.few_smem_set[kOut][kIdx], kern, kSmemPerSm - 1024) != HQ_OK) return HQ_ERR_CUDA;
+  // K is shared by a cluster until the CTAs are about two to an SM (and none is left without a step);
+  // the ring of an SM's CTAs together fills its shared memory.
+  const int kc = (int)ceil_div(p.K, hq::kMmK);
+  const long long token_tiles = ceil_div(p.T, kTokens), tiles = ceil_div(p.H, hq::kFewFeatures) * token_tiles * p.P;
+  int split = 1, split_log2 = 0;
+  while (split < hq::kFewMaxSplit && 2 * split <= kc && 2 * split * tiles <= 2 * d.sms) split *= 2, ++split_log2;
+  const size_t red = split > 1 ? hq::few_red_bytes(kTokens) : 0;
+  const int per_sm = (int)std::min<long long>(4, std::max<long long>(1, ceil_div(tiles * split, d.sms)));
+  const int fit = (int)((kSmemPerSm / per_sm - 2560 - 4 * kTokens - red) / hq::few_stage_bytes(kTokens));
+  const int stages = std::max(2, std::min({fit, hq::kFewMaxStages, (int)ceil_div(kc, split)}));
+  const size_t smem = 1024 + (size_t)stages * hq::few_stage_bytes(kTokens) + red;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(ceil_div(p.H, hq::kFewFeatures) * split), (unsigned)token_tiles, (unsigned)p.P);
+  cfg.blockDim = dim3(hq::kFewThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, map_a, map_w, p, split_log2, stages, wait_limits()) != cudaSuccess) {
+    cudaGetLastError();
+    return HQ_ERR_CUDA;
+  }
+  return HQ_OK;
+}
+
 template <int kOut>
 hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
   DeviceInfo* d = nullptr;
   if (device_info(&d) != HQ_OK) return HQ_ERR_CUDA;
   CUtensorMap map_a, map_w, map_out;
-  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, hq::kMmHalf, 128) ||
-      !encode_3d(&map_w, p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.H, p.P, p.ldw, hq::kMmHalf, 128))
-    return HQ_ERR_CUDA;
+  if (!encode_3d(&map_w, p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.H, p.P, p.ldw, hq::kMmHalf, 128)) return HQ_ERR_CUDA;
+  if (p.T <= 16) return launch_few<kOut, 16>(p, map_w, *d, st);
+  if (p.T <= 32) return launch_few<kOut, 32>(p, map_w, *d, st);
+  if (p.T <= 64) return launch_few<kOut, 64>(p, map_w, *d, st);
+  if (p.T <= 128) return launch_few<kOut, 128>(p, map_w, *d, st);
+  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, hq::kMmHalf, 128)) return HQ_ERR_CUDA;
   memset(&map_out, 0, sizeof map_out);
-  if (kOut == hq::kMmBf16 && !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.T, p.P, 2ull * p.ldo, 32, 64))
+  if (kOut == hq::kMmBf16 &&
+      !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.T, p.P, 2ull * p.ldo, 32, 64))
     return HQ_ERR_CUDA;
-  if (kOut == hq::kMmF32 && !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.H, p.T, p.P, 4ull * p.ldo, 32, 64))
+  if (kOut == hq::kMmF32 &&
+      !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.H, p.T, p.P, 4ull * p.ldo, 32, 64))
     return HQ_ERR_CUDA;
   auto kern = hq::int8_matmul_pair_kernel<kOut>;
   const size_t smem = sizeof(hq::MmSmem) + 1024;
-  {
-    std::lock_guard<std::mutex> lock(g_dev_mu);
-    if (!d->matmul_smem_set[kOut]) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return HQ_ERR_CUDA;
-      d->matmul_smem_set[kOut] = true;
-    }
-  }
+  if (raise_smem(d->pair_smem_set[kOut], kern, smem) != HQ_OK) return HQ_ERR_CUDA;
   const long long tiles = (long long)p.P * ceil_div(p.T, hq::kMmTile) * ceil_div(p.H, hq::kMmTile);
   const long long clusters = std::min<long long>(tiles, d->sms / 2);
   kern<<<(unsigned)(2 * clusters), hq::kMmThreads, smem, st>>>(map_a, map_w, map_out, p, wait_limits());

@@ -419,4 +419,242 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   if (warp == kMmEpiWarps + 1) tc_dealloc<2>(tmem, 512);
 }
 
+// ------------------------------------------------------------------------------------------------
+// Few tokens: a CTA, or a cluster of CTAs that share K, to 128 features and all tokens.
+//
+// With few tokens the product is bound by reading the weights once, so the weights are the M operand
+// (128 features a tile) and the tokens, padded to kTokens, the N operand: the accumulator's lane is a
+// feature and its column a token, and only as many columns as there are tokens are computed, loaded and
+// converted.  Where the feature tiles alone do not fill the GPU, the cluster's CTAs take a share of K
+// each and their int32 sums meet in distributed shared memory: CTA q adds up the columns q kTokens / S ..
+// of all S of them.  Sums of integers do not depend on the order.
+//
+// Warps 0-3 are the epilogue, warp 4 loads, warp 5 issues the products.
+constexpr int kFewFeatures = 128;
+constexpr int kFewThreads = 192;
+constexpr int kFewMaxStages = 8;
+constexpr int kFewMaxSplit = 8;
+
+__host__ __device__ constexpr unsigned few_stage_bytes(int tokens) { return kFewFeatures * kMmK + tokens * kMmK; }
+__host__ __device__ constexpr unsigned few_red_bytes(int tokens) { return kFewFeatures * tokens * 4; }
+
+// A lane's feature: its parameters, and where its results go.
+template <int kOut>
+struct FewFeature {
+  const MmArgs& p;
+  int r, n;  // rank, feature (compact position in the wire's order)
+  bool on;
+  float scale = 0.0f, second = 0.0f;
+  int zero = 0;
+
+  __device__ __forceinline__ FewFeature(const MmArgs& p, int r, int n) : p(p), r(r), n(n), on(n < p.H) {
+    if (!on) return;
+    const size_t g = (size_t)r * p.H + n;
+    scale = __ldg(p.w_scale + g);
+    if (kOut != kMmWire && p.bias) second = bf16_lo(__ldg(p.bias + g));
+    if (kOut == kMmWire && n < p.H - p.k) {
+      const size_t h = (size_t)r * p.H + checked_col(p.rest_idx, n, p.H);
+      second = __ldg(p.inv_scale + h);
+      zero = __ldg(p.zero + h);
+    }
+  }
+
+  // `count` (at most 8) tokens from t on, whose sums are acc and whose scales lie at sa.  All lanes of a
+  // warp hold neighbouring features and call together.
+  __device__ __forceinline__ void emit(const uint32_t (&acc)[8], int t, int count, const float* sa) {
+    const int lane = threadIdx.x & 31, Hr = p.H - p.k;
+    count = min(count, p.T - t);
+    if (count <= 0) return;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = __fmul_rn(__fmul_rn(__int2float_rn((int)acc[j]), j < count ? sa[j] : 0.0f), scale);
+      if (kOut != kMmWire && p.bias) v[j] = __fadd_rn(v[j], second);
+    }
+    if (kOut == kMmF32) {
+      float* o = static_cast<float*>(p.out) + ((size_t)r * p.T + t) * p.ldo + n;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (on && j < count) o[(size_t)j * p.ldo] = v[j];
+    } else if (kOut == kMmBf16) {
+      // two tokens at a time: an even lane takes the first token's features n, n + 1, an odd lane the
+      // second token's n - 1, n (H is a multiple of 8, so both are features or neither)
+      const bool odd = lane & 1;
+      uint16_t* o = static_cast<uint16_t*>(p.out) + ((size_t)r * p.T + t + odd) * p.ldo + (n - odd);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
+        const uint32_t w = odd ? pack_bf16x2(other, v[j + 1]) : pack_bf16x2(v[j], other);
+        if (on && j + odd < count) *reinterpret_cast<uint32_t*>(o + (size_t)j * p.ldo) = w;
+      }
+    } else {
+      // a token's code of this feature to nibble lane % 8, then 8 tokens x 8 lanes are exchanged so that
+      // lane i of 8 holds the whole word of token t + i
+      const int i = lane & 7;
+      uint32_t x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float b = bf16_lo(round_bf16x2(v[j], 0.0f));
+        const int c = __float2int_rn(__fmul_rn(b, second));  // saturating; NaN -> 0
+        x[j] = (uint32_t)(min(max(c, -zero), 15 - zero) + zero) << (4 * i);
+      }
+#pragma unroll
+      for (int step = 0; step < 3; ++step) {
+        const bool up = (i >> step) & 1;
+#pragma unroll
+        for (int j = 0; j < (4 >> step); ++j) {
+          const uint32_t keep = up ? x[2 * j + 1] : x[2 * j], give = up ? x[2 * j] : x[2 * j + 1];
+          x[j] = keep | __shfl_xor_sync(0xFFFFFFFFu, give, 1 << step);
+        }
+      }
+      if (n < Hr && i < count) p.codes[((size_t)r * p.T + t + i) * (Hr / 8) + (n >> 3)] = x[0];
+      if (on && n >= Hr) {
+        uint16_t* s = p.side + ((size_t)r * p.k + (n - Hr)) * p.T + t;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < count) s[j] = (uint16_t)pack_bf16x2(v[j], 0.0f);
+      }
+    }
+  }
+};
+
+template <int kOut, int kTokens>
+__global__ void __launch_bounds__(kFewThreads)
+    int8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                           const MmArgs p, int split_log2, int stages, WaitLimits lim) {
+  extern __shared__ unsigned char s_raw[];
+  __shared__ uint64_t s_full[kFewMaxStages], s_empty[kFewMaxStages], s_acc;
+  __shared__ float s_scale[kTokens];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  unsigned char* const base =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  int* const red = reinterpret_cast<int*>(base + stages * few_stage_bytes(kTokens));  // [split][kTokens / split][128]
+  constexpr uint32_t kColumns = kTokens < 32 ? 32 : kTokens;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int split = 1 << split_log2;
+  const int rank = split > 1 ? (int)cluster_ctarank() : 0;
+  const int n0 = (int)(blockIdx.x >> split_log2) * kFewFeatures, t0 = blockIdx.y * kTokens, r = blockIdx.z;
+  const int kc = (p.K + kMmK - 1) / kMmK;
+  const int c0 = (kc * rank) >> split_log2, c1 = (kc * (rank + 1)) >> split_log2;
+  volatile int* abort = &s_abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_empty[s], 1);
+    }
+    mbar_init(&s_acc, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 5) tc_alloc<1>(&s_tmem, kColumns);
+  if (warp == 4 && lane == 0) {
+    prefetch_tensor_map(&map_a);
+    prefetch_tensor_map(&map_w);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) cluster_arrive();  // here: this CTA's memory may be written
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 4) {  // ---------------------------------------------------------- loads
+    if (lane == 0) {
+      producer_start_delay(lim.start_delay);
+      int s = 0, phase = 1, issued = 0;
+      for (int c = c0; c < c1; ++c, ++issued) {
+        if (issued >= stages && !mbar_wait(&s_empty[s], phase, abort, lim.producer)) break;
+        unsigned char* at = base + s * few_stage_bytes(kTokens);
+        mbar_arrive_expect_tx(&s_full[s], few_stage_bytes(kTokens));
+        tma_load_3d(smem_addr(at), &map_w, c * kMmK, n0, r, smem_addr(&s_full[s]));
+        tma_load_3d(smem_addr(at + kFewFeatures * kMmK), &map_a, c * kMmK, t0, r, smem_addr(&s_full[s]));
+        if (++s == stages) s = 0, phase ^= 1;
+      }
+      if (*abort) {  // the loads in flight have landed before the CTA leaves
+        int ignore = 0;
+        for (int j = max(0, issued - stages); j < issued; ++j)
+          mbar_wait(&s_full[j % stages], (j / stages) & 1, &ignore, lim.producer);
+      }
+    }
+  } else if (warp == 5) {  // ---------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc_idesc(kFewFeatures, kTokens);
+      int s = 0, phase = 0;
+      for (int c = c0; c < c1; ++c) {
+        if (!mbar_wait(&s_full[s], phase, abort, lim.consumer)) break;
+        tc_fence_after();
+        const uint32_t at = smem_addr(base + s * few_stage_bytes(kTokens));
+        const uint64_t dw = tc_desc(at), da = tc_desc(at + kFewFeatures * kMmK);
+#pragma unroll
+        for (int k = 0; k < kMmK / 32; ++k) tc_mma<1>(tmem, dw + 2 * k, da + 2 * k, idesc, c > c0 || k > 0);
+        tc_commit<1>(&s_empty[s]);
+        if (++s == stages) s = 0, phase ^= 1;
+      }
+      tc_commit<1>(&s_acc);  // also after an abort: the products in flight are done before tensor memory is freed
+      int ignore = 0;
+      if (*abort) mbar_wait(&s_acc, 0, &ignore, lim.producer);
+    }
+  }
+  FewFeature<kOut> feature(p, r, warp < 4 ? n0 + 32 * warp + lane : p.H);
+  const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  bool ok = true;
+  if (warp < 4) {  // ------------------------------------------------------------ epilogue
+    for (int j = threadIdx.x; j < kTokens; j += 128)
+      s_scale[j] = t0 + j < p.T ? __ldg(p.a_scale + (size_t)r * p.T + t0 + j) : 0.0f;
+    named_barrier_sync(128);
+    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_acc, 0, abort, lim.consumer)) && !*abort;
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    tc_fence_after();
+    if (ok && split == 1) {
+#pragma unroll 1
+      for (int j = 0; j < kTokens; j += 8) {
+        uint32_t v[8];
+        tc_load(acc + j, v);
+        feature.emit(v, t0 + j, 8, s_scale + j);
+      }
+    } else if (ok) {
+      // the columns go to the CTAs that add them up
+      constexpr int kTokensLog2 = kTokens == 16 ? 4 : kTokens == 32 ? 5 : kTokens == 64 ? 6 : 7;
+      const int width_log2 = kTokensLog2 - split_log2;
+      const uint32_t mine = smem_addr(red + ((rank << width_log2) * kFewFeatures + threadIdx.x));
+#pragma unroll 1
+      for (int j = 0; j < kTokens; j += 8) {
+        uint32_t v[8];
+        tc_load(acc + j, v);
+        if (j == 0) cluster_wait();  // every CTA of the cluster is there
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int q = (j + i) >> width_log2, c = (j + i) & ((1 << width_log2) - 1);
+          st_cluster(cluster_addr(mine + c * kFewFeatures * 4, q), v[i]);
+        }
+      }
+    }
+  }
+  if (split > 1 && (warp >= 4 || !ok)) cluster_wait();
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) {
+    cluster_sync();  // all parts of this CTA's columns are here
+    if (warp < 4 && ok) {
+      const int width = kTokens >> split_log2;
+#pragma unroll 1
+      for (int c = 0; c < width; c += 8) {
+        uint32_t v[8] = {};
+#pragma unroll 2
+        for (int q = 0; q < split; ++q) {
+          const uint32_t at = smem_addr(red) + 4 * ((q * width + c) * kFewFeatures + threadIdx.x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < width) v[i] += ld_shared(at + 4 * i * kFewFeatures);
+        }
+        feature.emit(v, t0 + rank * width + c, width - c, s_scale + rank * width + c);
+      }
+    }
+  }
+  tc_fence_after();
+  if (warp == 5) tc_dealloc<1>(tmem, kColumns);
+}
+
 }  // namespace hq

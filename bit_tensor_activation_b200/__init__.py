@@ -109,8 +109,14 @@ def hq_wire_bytes_per_row(H: int, k: int) -> int:
     return int(_lib.hq_wire_bytes_per_row(H, k))
 
 
+# The current stream's handle without the Python object around it, where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device):
     if stream is None:
+        if _raw_stream is not None and device is not None and device.index is not None:
+            return _raw_stream(device.index)
         return torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -120,6 +126,8 @@ def _stream(stream, device):
 def _ptr(t, dtypes, shape, name):
     if t is None:
         return None
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return t.data_ptr() if t.numel() else None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -341,72 +349,99 @@ def hq_compress_reduce_ld(x, keep_idx, rest_idx, scale, inv_scale, zero, out, co
 _I8 = (torch.int8,)
 
 
-def _call(fn, where, device, others, args, stream):
-    """One call of the library on `device`, where every tensor lies, whatever device is current."""
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError(f"{where}: tensors on {device} and {t.device}")
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(stream, device))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(stream, device))
-    if st != HQ_OK:
-        raise HQError(st, where)
+def _dense(t, dev, dtypes, shape, name):
+    """Pointer of a contiguous tensor on device `dev`, or None for None: _ptr with the device checked."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    p = _ptr(t, dtypes, shape, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} lies on {t.device}, the first tensor on cuda:{dev}")
+    return p
 
 
-def _pitched(t, dtypes, shape, multiple, name):
-    """(pointer, row pitch in elements) of a tensor [..., n] whose rows are dense and one pitch apart.
-    The strides of dimensions of one element do not count; a tensor of at most one row has the pitch
-    of its width rounded up to `multiple`."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _pitched(t, dev, dtypes, shape, multiple, name):
+    """(pointer, row pitch in elements) of a tensor [..., n] on device `dev` whose rows are dense and one
+    pitch apart.  The strides of dimensions of one element do not count; a tensor of at most one row
+    has the pitch of its width rounded up to `multiple`."""
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
+    n = shape[-1]
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and n % multiple == 0 and t.is_contiguous():
+        return t.data_ptr(), n
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} lies on {t.device}, the first tensor on cuda:{dev}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.numel():
-        return None, -(-shape[-1] // multiple) * multiple
+        return None, -(-n // multiple) * multiple
     st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
+    if st[-1] != 1 and n > 1:
         raise ValueError(f"{name}: rows must be dense")
     ld, rows = None, 1
-    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
-        if n > 1:
+    for n_, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n_ > 1:
             if ld is None:
                 ld = s
             elif s != rows * ld:
                 raise ValueError(f"{name}: rows must be one pitch apart")
-            rows *= n
-    return t.data_ptr(), -(-shape[-1] // multiple) * multiple if ld is None else ld
+            rows *= n_
+    return t.data_ptr(), -(-n // multiple) * multiple if ld is None else ld
+
+
+def _device_of(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _call(fn, where, dev, stream, *args):
+    """One call of the library on device `dev`, whatever device is current."""
+    if stream is None and _raw_stream is not None:
+        stream = _raw_stream(dev)
+    else:
+        stream = _stream(stream, torch.device("cuda", dev))
+    if dev == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != HQ_OK:
+        raise HQError(st, where)
 
 
 def hq_quantize_tokens(x, q, scale, stream=None) -> None:
     """x [..., K] bf16 to int8 q [..., K] with one scale a row, scale [...] f32; the rows of x and q
     may be further apart than K (multiples of 8 and 16 elements)."""
-    *lead, K = x.shape
-    rows = 1
+    dev = _device_of(x, "x")
+    shape = x.shape
+    lead, rows = shape[:-1], 1
     for n in lead:
         rows *= n
-    px, ldx = _pitched(x, _BF16, (*lead, K), 8, "x")
-    pq, ldq = _pitched(q, _I8, (*lead, K), 16, "q")
-    _call(_lib.hq_quantize_tokens, "hq_quantize_tokens", x.device, (q, scale),
-          (px, ldx, rows, K, pq, ldq, _ptr(scale, _F32, tuple(lead), "scale")), stream)
+    px, ldx = _pitched(x, dev, _BF16, shape, 8, "x")
+    pq, ldq = _pitched(q, dev, _I8, shape, 16, "q")
+    _call(_lib.hq_quantize_tokens, "hq_quantize_tokens", dev, stream, px, ldx, rows, shape[-1], pq, ldq,
+          _dense(scale, dev, _F32, lead, "scale"))
 
 
 def hq_int8_matmul(a, a_scale, w, w_scale, out, bias=None, stream=None) -> None:
     """Every rank's partial sum out [P, T, H] (bf16 or f32) of int8 activations a [P, T, K] with a
     scale a token (a_scale [P, T]) and int8 weights w [P, H, K] with a scale a channel (w_scale
     [P, H]); bias [P, H] bf16.  The rows of a, w and out may be further apart than K and H."""
+    dev = _device_of(a, "a")
     P, T, K = a.shape
     H = w.shape[1]
-    pa, lda = _pitched(a, _I8, (P, T, K), 16, "a")
-    pw, ldw = _pitched(w, _I8, (P, H, K), 16, "w")
-    po, ldo = _pitched(out, _BF16 + _F32, (P, T, H), 8, "out")
-    _call(_lib.hq_int8_matmul, "hq_int8_matmul", a.device, (a_scale, w, w_scale, bias, out),
-          (pa, lda, _ptr(a_scale, _F32, (P, T), "a_scale"), pw, ldw, _ptr(w_scale, _F32, (P, H), "w_scale"),
-           _ptr(bias, _BF16, (P, H), "bias"), P, T, H, K, po, ldo,
-           HQ_OUT_F32 if out.dtype == torch.float32 else HQ_OUT_BF16), stream)
+    pa, lda = _pitched(a, dev, _I8, (P, T, K), 16, "a")
+    pw, ldw = _pitched(w, dev, _I8, (P, H, K), 16, "w")
+    po, ldo = _pitched(out, dev, _BF16 + _F32, (P, T, H), 8, "out")
+    _call(_lib.hq_int8_matmul, "hq_int8_matmul", dev, stream, pa, lda, _dense(a_scale, dev, _F32, (P, T), "a_scale"), pw,
+          ldw, _dense(w_scale, dev, _F32, (P, H), "w_scale"), _dense(bias, dev, _BF16, (P, H), "bias"), P, T, H, K, po,
+          ldo, HQ_OUT_F32 if out.dtype == torch.float32 else HQ_OUT_BF16)
 
 
 def hq_int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, zero, codes, side,
@@ -414,17 +449,17 @@ def hq_int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, z
     """The wire (codes, side) of the partial sums that hq_int8_matmul would write, bit for bit as
     hq_quantize_pack makes it.  w and w_scale have their rows in the wire's order:
     torch.cat([rest_idx, keep_idx]) of the features' own."""
+    dev = _device_of(a, "a")
     P, T, K = a.shape
     H = w.shape[1]
     k = keep_idx.shape[0]
-    pa, lda = _pitched(a, _I8, (P, T, K), 16, "a")
-    pw, ldw = _pitched(w, _I8, (P, H, K), 16, "w")
-    _call(_lib.hq_int8_matmul_pack, "hq_int8_matmul_pack", a.device,
-          (a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, zero, codes, side),
-          (pa, lda, _ptr(a_scale, _F32, (P, T), "a_scale"), pw, ldw, _ptr(w_scale, _F32, (P, H), "w_scale"), P, T, H, K,
-           k, _ptr(keep_idx, _I32, (k,), "keep_idx"), _ptr(rest_idx, _I32, (H - k,), "rest_idx"),
-           _ptr(inv_scale, _F32, (P, H), "inv_scale"), _ptr(zero, _U8, (P, H), "zero"),
-           _ptr(codes, _CODES, (P, T, (H - k) // 8), "codes"), _ptr(side, _BF16, (P, k, T), "side")), stream)
+    pa, lda = _pitched(a, dev, _I8, (P, T, K), 16, "a")
+    pw, ldw = _pitched(w, dev, _I8, (P, H, K), 16, "w")
+    _call(_lib.hq_int8_matmul_pack, "hq_int8_matmul_pack", dev, stream, pa, lda,
+          _dense(a_scale, dev, _F32, (P, T), "a_scale"), pw, ldw, _dense(w_scale, dev, _F32, (P, H), "w_scale"), P, T, H,
+          K, k, _dense(keep_idx, dev, _I32, (k,), "keep_idx"), _dense(rest_idx, dev, _I32, (H - k,), "rest_idx"),
+          _dense(inv_scale, dev, _F32, (P, H), "inv_scale"), _dense(zero, dev, _U8, (P, H), "zero"),
+          _dense(codes, dev, _CODES, (P, T, (H - k) // 8), "codes"), _dense(side, dev, _BF16, (P, k, T), "side"))
 
 
 def hq_residual_norm(y, res, res_out, h=None, q=None, q_scale=None, post=HQ_NORM_NONE, post_w=None, post_b=None,
@@ -434,24 +469,25 @@ def hq_residual_norm(y, res, res_out, h=None, q=None, q_scale=None, post=HQ_NORM
     int8 with one scale a row (q, q_scale).  y, res, res_out, h [T, H] (y and res bf16 or f32; res_out
     of res's type, res itself allowed); q [T, H] int8, rows may be further apart; weights and biases
     [H] f32; gate [G, H] bf16 with G a divisor of T: row t uses gate row t // (T // G)."""
-    T, H = y.shape
-    gate_rows = 0
+    dev = _device_of(y, "y")
+    T, H = shape = y.shape
+    vector = (H,)
+    gate_rows, pg = 0, None
     if gate is not None:
         G = gate.shape[0]
         if G < 1 or T % G:
             raise ValueError(f"gate: {G} rows do not divide {T}")
-        gate_rows = max(T // G, 1)
-    if res.dtype != res_out.dtype and torch.float32 in (res.dtype, res_out.dtype):
+        gate_rows, pg = max(T // G, 1), _dense(gate, dev, _BF16, (G, H), "gate")
+    f32 = res.dtype == torch.float32
+    if f32 != (res_out.dtype == torch.float32):
         raise TypeError("res and res_out must have the same type")
-    pq, ldq = (None, 0) if q is None else _pitched(q, _I8, (T, H), 16, "q")
-    _call(_lib.hq_residual_norm, "hq_residual_norm", y.device,
-          (res, res_out, h, q, q_scale, post_w, post_b, gate, pre_w, pre_b),
-          (_ptr(y, _BF16 + _F32, (T, H), "y"), HQ_OUT_F32 if y.dtype == torch.float32 else HQ_OUT_BF16,
-           _ptr(res, _BF16 + _F32, (T, H), "res"), _ptr(res_out, _BF16 + _F32, (T, H), "res_out"),
-           HQ_OUT_F32 if res.dtype == torch.float32 else HQ_OUT_BF16, T, H, post, _ptr(post_w, _F32, (H,), "post_w"),
-           _ptr(post_b, _F32, (H,), "post_b"), None if gate is None else _ptr(gate, _BF16, (G, H), "gate"), gate_rows,
-           float(alpha), float(beta), pre, _ptr(pre_w, _F32, (H,), "pre_w"), _ptr(pre_b, _F32, (H,), "pre_b"),
-           float(eps), _ptr(h, _BF16, (T, H), "h"), pq, ldq, _ptr(q_scale, _F32, (T,), "q_scale")), stream)
+    pq, ldq = (None, 0) if q is None else _pitched(q, dev, _I8, shape, 16, "q")
+    _call(_lib.hq_residual_norm, "hq_residual_norm", dev, stream, _dense(y, dev, _BF16 + _F32, shape, "y"),
+          HQ_OUT_F32 if y.dtype == torch.float32 else HQ_OUT_BF16, _dense(res, dev, _BF16 + _F32, shape, "res"),
+          _dense(res_out, dev, _BF16 + _F32, shape, "res_out"), HQ_OUT_F32 if f32 else HQ_OUT_BF16, T, H, post,
+          _dense(post_w, dev, _F32, vector, "post_w"), _dense(post_b, dev, _F32, vector, "post_b"), pg, gate_rows,
+          alpha, beta, pre, _dense(pre_w, dev, _F32, vector, "pre_w"), _dense(pre_b, dev, _F32, vector, "pre_b"), eps,
+          _dense(h, dev, _BF16, shape, "h"), pq, ldq, _dense(q_scale, dev, _F32, (T,), "q_scale"))
 
 
 def hq_selftest_bounded_wait(limit_cycles: int, stream=None, device=None) -> None:

@@ -57,6 +57,7 @@ struct DeviceInfo {
   int qt_blocks = 0;
   bool select_smem_set = false;
   bool pair_smem_set[3] = {};        // [output]
+  bool norm_smem_set[2][2][2] = {};  // [fp32 y][fp32 residual][threads all full]
   bool few_smem_set[3][4] = {};      // [output][tokens 16, 32, 64, 128]
   OccupancyCache dequant_tma[2][2];  // [fp32 out][bf16 shards]
   OccupancyCache dequant_cp[2][2];
@@ -636,20 +637,41 @@ hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
 }
 
 template <typename Y, typename R>
-hq_status launch_norm(const hq::NormArgs& a, cudaStream_t st) {
+hq_status launch_norm(const hq::NormArgs& a, DeviceInfo& d, cudaStream_t st) {
   const RowShape s = row_shape(a.H);
-  const unsigned grid = (unsigned)(s.warp ? ceil_div(a.T, 4) : a.T);
-#define HQ_ROWS(NV, W) hq::residual_norm_kernel<Y, R, NV, W><<<grid, s.threads, 0, st>>>(a)
   if (s.warp) {
-    if (s.nv == 1) HQ_ROWS(1, true);
-    else if (s.nv == 2) HQ_ROWS(2, true);
-    else HQ_ROWS(4, true);
-  } else {
-    if (s.nv == 1) HQ_ROWS(1, false);
-    else if (s.nv == 2) HQ_ROWS(2, false);
-    else HQ_ROWS(4, false);
+    const unsigned grid = (unsigned)ceil_div(a.T, 4);
+    if (s.nv == 1) hq::residual_norm_kernel<Y, R, 1, 128, true><<<grid, 128, 0, st>>>(a);
+    else if (s.nv == 2) hq::residual_norm_kernel<Y, R, 2, 128, true><<<grid, 128, 0, st>>>(a);
+    else hq::residual_norm_kernel<Y, R, 4, 128, true><<<grid, 128, 0, st>>>(a);
+    return launched();
   }
-#undef HQ_ROWS
+  const int nvec = a.H / 8;
+  auto threads = [&](int nv) { return (int)(32 * ceil_div(ceil_div(nvec, nv), 32)); };
+  // Which kernel, by what was measured (bf16, gate, both weights): the row ring from 4096 < H <= 8192 and
+  // eight rows an SM on (8192 x 8192: 99 us, a CTA a row 120; 1500 x 8192: 25.6 and 26.1; 777 x 8192: 16.9
+  // and 16.1; 4096 x 4096: 33.4 and 32.0); below two rows an SM one vector a thread (148 x 8192: 5.2 us,
+  // two vectors 5.5; 300 x 8192: 11.9 and 9.1).
+  if (nvec > hq::kRowsThreads && nvec <= hq::kRowsVec * hq::kRowsThreads && !a.post_b && !a.pre_b && a.T >= 8 * d.sms) {
+    const int nt = threads(hq::kRowsVec);
+    const bool full = a.H == 8 * hq::kRowsVec * nt;
+    auto kern = full ? hq::residual_norm_rows_kernel<Y, R, true> : hq::residual_norm_rows_kernel<Y, R, false>;
+    const size_t row = (size_t)a.H * (sizeof(Y) + sizeof(R));
+    const int stages = (int)std::min<size_t>(hq::kRowsMaxStages, (kSmemPerSm - 2048) / row);
+    if (raise_smem(d.norm_smem_set[sizeof(Y) == 4][sizeof(R) == 4][full], kern, kSmemPerSm - 2048) != HQ_OK)
+      return HQ_ERR_CUDA;
+    kern<<<(unsigned)d.sms, nt, stages * row, st>>>(a, stages, wait_limits());
+    return launched();
+  }
+  if (nvec > 2 * hq::kRowMaxThreads) {
+    hq::residual_norm_kernel<Y, R, 4, 1024, false><<<a.T, threads(4), 0, st>>>(a);
+  } else if (nvec > hq::kRowMaxThreads) {
+    hq::residual_norm_kernel<Y, R, 4, 512, false><<<a.T, threads(4), 0, st>>>(a);
+  } else if (a.T >= 2 * d.sms) {
+    hq::residual_norm_kernel<Y, R, 2, 512, false><<<a.T, threads(2), 0, st>>>(a);
+  } else {
+    hq::residual_norm_kernel<Y, R, 1, 1024, false><<<a.T, threads(1), 0, st>>>(a);
+  }
   return launched();
 }
 
@@ -862,10 +884,13 @@ hq_status hq_residual_norm(const void* y, hq_out_dtype y_dtype, const void* res,
   if (T == 0) return HQ_OK;
   hq::NormArgs a{y, res, res_out, T, H, (int)post, (int)pre, post_w, post_b, gate, gate ? gate_rows : 1, alpha, beta,
                  pre_w, pre_b, eps, h, q, ldq, q_scale};
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != HQ_OK) return HQ_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   if (y_dtype == HQ_OUT_BF16)
-    return res_dtype == HQ_OUT_BF16 ? launch_norm<uint16_t, uint16_t>(a, st) : launch_norm<uint16_t, float>(a, st);
-  return res_dtype == HQ_OUT_BF16 ? launch_norm<float, uint16_t>(a, st) : launch_norm<float, float>(a, st);
+    return res_dtype == HQ_OUT_BF16 ? launch_norm<uint16_t, uint16_t>(a, *d, st)
+                                    : launch_norm<uint16_t, float>(a, *d, st);
+  return res_dtype == HQ_OUT_BF16 ? launch_norm<float, uint16_t>(a, *d, st) : launch_norm<float, float>(a, *d, st);
 }
 
 const char* hq_status_string(hq_status s) {

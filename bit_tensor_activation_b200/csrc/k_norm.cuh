@@ -11,6 +11,7 @@
 #pragma once
 
 #include "hq_rows.cuh"
+#include "hq_tma.cuh"
 
 namespace hq {
 
@@ -34,73 +35,142 @@ struct NormArgs {
   float* q_scale;
 };
 
+// Eight values as they lie in memory, and as floats.
 template <typename T>
-__device__ __forceinline__ void load_vec8(const void* base, size_t at, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 v = ld_stream16(static_cast<const uint16_t*>(base) + at);
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const void* base, size_t at) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = bf16_at(v, i);
-  } else {
-    const uint4 a = ld_stream16(static_cast<const float*>(base) + at);
-    const uint4 b = ld_stream16(static_cast<const float*>(base) + at + 4);
-    f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
-    f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+      v[i] = ld_stream16(static_cast<const char*>(base) + at * sizeof(T) + 16 * i);
   }
-}
-__device__ __forceinline__ void load_param8(const float* __restrict__ p, int at, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p + at));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p + at) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 2) return bf16_at(v[0], i);
+    const uint4& q = v[i / 4];
+    return __uint_as_float((i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w);
+  }
+};
+// Pairs of neighbouring values throughout, for the instructions that take two at once: v[c][p] are
+// elements 2p, 2p + 1 of vector c.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+template <typename T>
+__device__ __forceinline__ float2 pair_of(const Raw8<T>& r, int p) { return make_float2(r.at(2 * p), r.at(2 * p + 1)); }
+__device__ __forceinline__ Raw8<uint16_t> round_pairs(const float2 (&v)[4]) {
+  return Raw8<uint16_t>{{make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                                    pack_bf16x2(v[3].x, v[3].y))}};
 }
 
-// The norm of the row in v, in place: kind is the same for all threads.
-template <int NV, bool kWarpRow>
-__device__ __forceinline__ void norm_row(RowGroup<kWarpRow>& g, float (&v)[NV][8], int kind, const float* w,
-                                         const float* b, float eps, int H, int i, int nt) {
-  const float inv_n = __fdiv_rn(1.0f, (float)H);
-  float mean = 0.0f;
+// The row in v less its mean (a layer norm's) and 1 / sqrt(mean square + eps) of what is then there.  Bit
+// c of `in`: vector c lies within the row (kFull: all do); the others hold 0 and stay 0.
+template <int NV, bool kFull, bool kWarpRow>
+__device__ __forceinline__ float centre_row(RowGroup<kWarpRow>& g, float2 (&v)[NV][4], int kind, float eps, float inv_n,
+                                            uint32_t in) {
+  float2 s = both(0.0f);
   if (kind == HQ_NORM_LAYER) {
-    float s = 0.0f;
 #pragma unroll
     for (int c = 0; c < NV; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = __fadd_rn(s, v[c][e]);
-    mean = __fmul_rn(g.sum(s), inv_n);
-  }
-  float s = 0.0f;
+      for (int p = 0; p < 4; ++p) s = __fadd2_rn(s, v[c][p]);
+    const float mean = __fmul_rn(g.sum(__fadd_rn(s.x, s.y)), inv_n);
+    s = both(0.0f);
 #pragma unroll
-  for (int c = 0; c < NV; ++c) {
-    if (8 * (i + c * nt) >= H) continue;
+    for (int c = 0; c < NV; ++c) {
+      const float2 m = both(kFull || ((in >> c) & 1u) ? -mean : 0.0f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[c][e] = __fadd_rn(v[c][e], -mean);
-      s = __fmaf_rn(v[c][e], v[c][e], s);
+      for (int p = 0; p < 4; ++p) v[c][p] = __fadd2_rn(v[c][p], m);
     }
   }
-  const float rstd = __frsqrt_rn(__fmaf_rn(g.sum(s), inv_n, eps));
 #pragma unroll
-  for (int c = 0; c < NV; ++c) {
-    const int at = 8 * (i + c * nt);
-    if (at >= H) continue;
-    float f[8];
-    if (w) {
-      load_param8(w, at, f);
+  for (int c = 0; c < NV; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] = __fmul_rn(__fmul_rn(v[c][e], rstd), f[e]);
-    } else {
+    for (int p = 0; p < 4; ++p) s = __ffma2_rn(v[c][p], v[c][p], s);
+  return __frsqrt_rn(__fmaf_rn(g.sum(__fadd_rn(s.x, s.y)), inv_n, eps));
+}
+
+// The norm of the row in v, in place, weight and bias from memory.  `at` are the places of the thread's
+// vectors, moved back into the row where they lie past its end: what is computed there is finite work on
+// nothing that is kept, and these loops have no condition in them.
+template <int NV, bool kWarpRow>
+__device__ __forceinline__ void norm_row(RowGroup<kWarpRow>& g, float2 (&v)[NV][4], int kind, const float* w,
+                                         const float* b, float eps, int H, const int (&at)[NV], uint32_t in) {
+  const float2 rstd = both(centre_row<NV, false, kWarpRow>(g, v, kind, eps, __fdiv_rn(1.0f, (float)H), in));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] = __fmul_rn(v[c][e], rstd);
-    }
-    if (b) {
-      load_param8(b, at, f);
+  for (int c = 0; c < NV; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] = __fadd_rn(v[c][e], f[e]);
-    }
+    for (int p = 0; p < 4; ++p) v[c][p] = __fmul2_rn(v[c][p], rstd);
+  if (w) {
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int p = 0; p < 4; p += 2) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(w + at[c] + 2 * p));
+        v[c][p] = __fmul2_rn(v[c][p], make_float2(f.x, f.y));
+        v[c][p + 1] = __fmul2_rn(v[c][p + 1], make_float2(f.z, f.w));
+      }
+  }
+  if (b) {
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int p = 0; p < 4; p += 2) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(b + at[c] + 2 * p));
+        v[c][p] = __fadd2_rn(v[c][p], make_float2(f.x, f.y));
+        v[c][p + 1] = __fadd2_rn(v[c][p + 1], make_float2(f.z, f.w));
+      }
   }
 }
 
-template <typename Y, typename R, int NV, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 128 : kRowMaxThreads) residual_norm_kernel(const NormArgs a) {
+// The new residual of one vector, stored if `here`, and back in v as it was stored (0 where it is another
+// thread's).
+template <typename R>
+__device__ __forceinline__ void residual8(const NormArgs& a, const Raw8<R>& r, float2 (&v)[4], size_t at, bool in, bool here) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) v[p] = __ffma2_rn(both(a.alpha), pair_of(r, p), __fmul2_rn(both(a.beta), v[p]));
+  if constexpr (sizeof(R) == 2) {
+    const Raw8<uint16_t> o = round_pairs(v);
+    if (here) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.res_out) + at) = o.v[0];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) v[p] = pair_of(o, p);
+  } else if (here) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.res_out) + at);
+    o[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    o[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  }
+  if (!in) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) v[p] = both(0.0f);
+  }
+}
+__device__ __forceinline__ void gate8(const uint4& gate, float2 (&v)[4]) {
+  const Raw8<uint16_t> w{{gate}};
+#pragma unroll
+  for (int p = 0; p < 4; ++p) v[p] = __fmul2_rn(v[p], pair_of(w, p));
+}
+
+// The normed row out: as bf16, and its codes, which are those of quantize_tokens on that bf16 row.
+template <int NV, bool kFull, bool kWarpRow>
+__device__ __forceinline__ void store_row(RowGroup<kWarpRow>& g, const NormArgs& a, const float2 (&v)[NV][4], int row,
+                                          const int (&at)[NV], uint32_t in, bool first, bool ok) {
+  uint4 o[NV];
+  uint32_t m = 0;
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    o[c] = round_pairs(v[c]).v[0];
+    if (!kFull && !((in >> c) & 1u)) continue;
+    m = amax_bits(o[c], m);
+    if (a.h && ok) *reinterpret_cast<uint4*>(a.h + (size_t)row * a.H + at[c]) = o[c];
+  }
+  if (!a.q) return;
+  const RowScale s = row_scale(g.max_u32(max(m & 0xFFFFu, m >> 16)));
+  if (first && ok) a.q_scale[row] = s.scale;
+#pragma unroll
+  for (int c = 0; c < NV; ++c)
+    if ((kFull || ((in >> c) & 1u)) && ok)
+      store_codes8(a.q + (size_t)row * a.ldq, at[c] / 8, a.H, codes8(o[c], s.inv));
+}
+
+template <typename Y, typename R, int NV, int kMaxThreads, bool kWarpRow>
+__global__ void __launch_bounds__(kMaxThreads) residual_norm_kernel(const NormArgs a) {
   __shared__ float s_red[2 * kRowMaxWarps];
   RowGroup<kWarpRow> g{s_red, 0};
   const int i = kWarpRow ? (threadIdx.x & 31) : threadIdx.x;
@@ -109,63 +179,166 @@ __global__ void __launch_bounds__(kWarpRow ? 128 : kRowMaxThreads) residual_norm
   if (kWarpRow && row >= a.T) return;
   const int H = a.H;
   const size_t base = (size_t)row * H;
-  float v[NV][8], r[NV][8];
+  int at[NV];
+  uint32_t in = 0;
+  Raw8<Y> y[NV];
+  Raw8<R> r[NV];
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
-    const int at = 8 * (i + c * nt);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[c][e] = r[c][e] = 0.0f;
-    if (at < H) {
-      load_vec8<Y>(a.y, base + at, v[c]);
-      load_vec8<R>(a.res, base + at, r[c]);
+    at[c] = 8 * (i + c * nt);
+    y[c] = Raw8<Y>{};
+    r[c] = Raw8<R>{};
+    if (at[c] < H) {
+      y[c].load(a.y, base + at[c]);
+      r[c].load(a.res, base + at[c]);
+      in |= 1u << c;
     }
+    at[c] = min(at[c], H - 8);
   }
-  if (a.post != HQ_NORM_NONE) norm_row<NV, kWarpRow>(g, v, a.post, a.post_w, a.post_b, a.eps, H, i, nt);
-  const uint16_t* gate = a.gate ? a.gate + (size_t)(row / a.gate_rows) * H : nullptr;
+  float2 v[NV][4];
 #pragma unroll
-  for (int c = 0; c < NV; ++c) {
-    const int at = 8 * (i + c * nt);
-    if (at >= H) continue;
-    if (gate) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(gate + at));
+  for (int c = 0; c < NV; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] = __fmul_rn(v[c][e], bf16_at(w, e));
-    }
+    for (int p = 0; p < 4; ++p) v[c][p] = pair_of(y[c], p);
+  if (a.post != HQ_NORM_NONE) norm_row<NV, kWarpRow>(g, v, a.post, a.post_w, a.post_b, a.eps, H, at, in);
+  if (a.gate) {
+    const uint16_t* gate = a.gate + (size_t)(a.gate_rows >= a.T ? 0 : row / a.gate_rows) * H;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[c][e] = __fmaf_rn(a.alpha, r[c][e], __fmul_rn(a.beta, v[c][e]));
-    if constexpr (sizeof(R) == 2) {
-      const uint4 o = make_uint4(pack_bf16x2(v[c][0], v[c][1]), pack_bf16x2(v[c][2], v[c][3]),
-                                 pack_bf16x2(v[c][4], v[c][5]), pack_bf16x2(v[c][6], v[c][7]));
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.res_out) + base + at) = o;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] = bf16_at(o, e);
-    } else {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.res_out) + base + at);
-      o[0] = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
-      o[1] = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
-    }
+    for (int c = 0; c < NV; ++c) gate8(__ldg(reinterpret_cast<const uint4*>(gate + at[c])), v[c]);
   }
+#pragma unroll
+  for (int c = 0; c < NV; ++c) residual8(a, r[c], v[c], base + at[c], (in >> c) & 1u, (in >> c) & 1u);
   if (a.pre == HQ_NORM_NONE) return;
-  norm_row<NV, kWarpRow>(g, v, a.pre, a.pre_w, a.pre_b, a.eps, H, i, nt);
-  // h as bf16, and its codes: exactly those of quantize_tokens on that bf16 row
-  uint4 o[NV];
-  uint32_t m = 0;
+  norm_row<NV, kWarpRow>(g, v, a.pre, a.pre_w, a.pre_b, a.eps, H, at, in);
+  store_row<NV, false, kWarpRow>(g, a, v, row, at, in, i == 0, true);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Many rows: one CTA an SM walks the rows, a ring of whole rows ahead of it.
+//
+// A thread keeps its 16 columns (two vectors) of the weights and of the gate in registers from row to
+// row: at H = 8192 a row's weights and gate are 80 KB beside its 64 KB of data, and reading them from L1
+// for every row, with a row's loads waited for at its start, held the one-CTA-a-row kernel above to half
+// of the memory's rate.  The rows come by bulk copies of H elements, counted by an mbarrier a stage; a
+// stage is refilled once every thread has taken its part of it (the first barrier of its row).
+constexpr int kRowsVec = 2;
+constexpr int kRowsThreads = 512;
+constexpr int kRowsMaxStages = 8;
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, unsigned bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+
+// The norm of the row in v with the weights in registers (w: all ones where there is none, no bias).
+template <bool kFull>
+__device__ __forceinline__ void norm_row_reg(RowGroup<false>& g, float2 (&v)[kRowsVec][4], int kind,
+                                             const float2 (&w)[kRowsVec][4], float eps, float inv_n, uint32_t in) {
+  const float2 rstd = both(centre_row<kRowsVec, kFull, false>(g, v, kind, eps, inv_n, in));
 #pragma unroll
-  for (int c = 0; c < NV; ++c) {
-    const int at = 8 * (i + c * nt);
-    o[c] = make_uint4(pack_bf16x2(v[c][0], v[c][1]), pack_bf16x2(v[c][2], v[c][3]), pack_bf16x2(v[c][4], v[c][5]),
-                      pack_bf16x2(v[c][6], v[c][7]));
-    if (at >= H) continue;
-    m = amax_bits(o[c], m);
-    if (a.h) *reinterpret_cast<uint4*>(a.h + base + at) = o[c];
+  for (int c = 0; c < kRowsVec; ++c)
+#pragma unroll
+    for (int p = 0; p < 4; ++p) v[c][p] = __fmul2_rn(__fmul2_rn(v[c][p], rstd), w[c][p]);
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw_from_shared(uint32_t at) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.v[i].x), "=r"(r.v[i].y), "=r"(r.v[i].z), "=r"(r.v[i].w)
+                 : "r"(at + 16 * i));
+  return r;
+}
+
+template <typename Y, typename R, bool kFull>
+__global__ void __launch_bounds__(kRowsThreads, 1) residual_norm_rows_kernel(const NormArgs a, int stages, WaitLimits lim) {
+  extern __shared__ __align__(128) unsigned char s_rows[];
+  __shared__ float s_red[2 * kRowMaxWarps];
+  __shared__ uint64_t s_full[kRowsMaxStages];
+  __shared__ int s_abort;
+  RowGroup<false> g{s_red, 0};
+  const int i = threadIdx.x, nt = blockDim.x, H = a.H;
+  const unsigned y_bytes = H * sizeof(Y), r_bytes = H * sizeof(R), stage_bytes = y_bytes + r_bytes;
+  const uint32_t ring = smem_addr(s_rows);
+  volatile int* abort = &s_abort;
+  if (i == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&s_full[s], 1);
+    s_abort = 0;
+    fence_barrier_init();
   }
-  if (!a.q) return;
-  const RowScale s = row_scale(g.max_u32(max(m & 0xFFFFu, m >> 16)));
-  if (i == 0) a.q_scale[row] = s.scale;
+  __syncthreads();
+  // thread 0 loads row `row` into stage s
+  auto load = [&](int row, int s) {
+    mbar_arrive_expect_tx(&s_full[s], stage_bytes);
+    bulk_load(ring + s * stage_bytes, static_cast<const Y*>(a.y) + (size_t)row * H, y_bytes, &s_full[s]);
+    bulk_load(ring + s * stage_bytes + y_bytes, static_cast<const R*>(a.res) + (size_t)row * H, r_bytes, &s_full[s]);
+  };
+  if (i == 0) {
+    producer_start_delay(lim.start_delay);
+    for (int s = 0, row = blockIdx.x; s < stages && row < a.T; ++s, row += gridDim.x) load(row, s);
+  }
+  int at[kRowsVec];
+  uint32_t in = 0;
+  float2 pw[kRowsVec][4], qw[kRowsVec][4];
+  uint4 gate[kRowsVec];
 #pragma unroll
-  for (int c = 0; c < NV; ++c) {
-    const int j = i + c * nt;
-    if (8 * j < H) store_codes8(a.q + (size_t)row * a.ldq, j, H, codes8(o[c], s.inv));
+  for (int c = 0; c < kRowsVec; ++c) {
+    at[c] = 8 * (i + c * nt);
+    if (at[c] < H) in |= 1u << c;
+    at[c] = min(at[c], H - 8);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      pw[c][p] = a.post_w ? __ldg(reinterpret_cast<const float2*>(a.post_w + at[c]) + p) : both(1.0f);
+      qw[c][p] = a.pre_w ? __ldg(reinterpret_cast<const float2*>(a.pre_w + at[c]) + p) : both(1.0f);
+    }
+  }
+  const float inv_n = __fdiv_rn(1.0f, (float)H);
+  int gate_row = -1, n = 0, s = 0, phase = 0;
+  bool ok = true;
+  for (int row = blockIdx.x; row < a.T; row += gridDim.x, ++n) {
+    if (a.gate) {
+      const int gr = a.gate_rows >= a.T ? 0 : row / a.gate_rows;
+      if (gr != gate_row) {
+        gate_row = gr;
+#pragma unroll
+        for (int c = 0; c < kRowsVec; ++c) gate[c] = __ldg(reinterpret_cast<const uint4*>(a.gate + (size_t)gr * H + at[c]));
+      }
+    }
+    // a wait that gives up leaves the barriers of the rows to come in step: nothing more is written
+    ok = mbar_wait(&s_full[s], phase, abort, lim.consumer) && ok;
+    Raw8<R> r[kRowsVec];
+    float2 v[kRowsVec][4];
+#pragma unroll
+    for (int c = 0; c < kRowsVec; ++c) {
+      const Raw8<Y> y = raw_from_shared<Y>(ring + s * stage_bytes + at[c] * (unsigned)sizeof(Y));
+      r[c] = raw_from_shared<R>(ring + s * stage_bytes + y_bytes + at[c] * (unsigned)sizeof(R));
+#pragma unroll
+      for (int p = 0; p < 4; ++p) v[c][p] = kFull || ((in >> c) & 1u) ? pair_of(y, p) : both(0.0f);
+    }
+    if (a.post != HQ_NORM_NONE) norm_row_reg<kFull>(g, v, a.post, pw, a.eps, inv_n, in);
+    else __syncthreads();
+    if (i == 0 && ok) {  // every thread has its part of the stage
+      const long long ahead = (long long)row + (long long)stages * gridDim.x;
+      if (ahead < a.T) load((int)ahead, s);
+    }
+    if (++s == stages) s = 0, phase ^= 1;
+    const size_t base = (size_t)row * H;
+#pragma unroll
+    for (int c = 0; c < kRowsVec; ++c) {
+      if (a.gate) gate8(gate[c], v[c]);
+      const bool mine = kFull || ((in >> c) & 1u);
+      residual8(a, r[c], v[c], base + at[c], mine, mine && ok);
+    }
+    if (a.pre == HQ_NORM_NONE) continue;
+    norm_row_reg<kFull>(g, v, a.pre, qw, a.eps, inv_n, in);
+    store_row<kRowsVec, kFull, false>(g, a, v, row, at, in, i == 0, ok);
+  }
+  if (i == 0 && *abort) {  // the copies in flight have landed before the CTA leaves
+    int ignore = 0;
+    for (int q = 0; q < stages; ++q) mbar_wait(&s_full[q], 0, &ignore, lim.producer);
   }
 }
 

@@ -519,3 +519,40 @@ def test_refusals():
         hq.hq_residual_norm(y, y, out[0])
     torch.cuda.synchronize()
     assert (out == 7).all()
+
+
+# -------------------------------------------------------------------------------- many rows to norm
+@pytest.mark.parametrize("T,H,kinds,gates", [(1184, 8192, ("rms", "rms"), 1), (1300, 4104, ("layer", "layer"), 0),
+                                             (1190, 5000, ("none", "rms"), 1190), (1200, 8192, ("rms", "none"), 3)])
+@pytest.mark.parametrize("y_t,r_t", [(BF, BF), (torch.float32, BF), (BF, torch.float32), (torch.float32, torch.float32)],
+                         ids=["bf16", "f32-bf16", "bf16-f32", "f32"])
+def test_residual_norm_of_many_rows(T, H, kinds, gates, y_t, r_t):
+    """Enough rows for the kernel that keeps weights in registers and rows in a ring."""
+    kind = {"none": hq.HQ_NORM_NONE, "rms": hq.HQ_NORM_RMS, "layer": hq.HQ_NORM_LAYER}
+    post, pre = kind[kinds[0]], kind[kinds[1]]
+    g = gen(T + H)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    y, res = (2 * rnd(T, H) + 0.5).to(y_t), rnd(T, H).to(r_t)
+    post_w, pre_w = 1 + rnd(H) / 4 if post else None, 1 + rnd(H) / 4 if pre else None
+    gate = torch.tanh(rnd(gates, H)).to(BF) if gates else None
+    buf = torch.full((T + 2, H), 7.0, dtype=r_t, device=DEV)
+    out = buf[1:T + 1]
+    h = torch.empty(T, H, dtype=BF, device=DEV) if pre else None
+    q, q_s = (torch.empty(T, up(H, 16), dtype=torch.int8, device=DEV)[:, :H], torch.empty(T, device=DEV)) if pre else (None, None)
+    hq.hq_residual_norm(y, res, out, h=h, q=q, q_scale=q_s, post=post, post_w=post_w, gate=gate, alpha=0.5, beta=2.0,
+                        pre=pre, pre_w=pre_w, eps=1e-5)
+    u, mag = plain_norm(y, post, post_w, None, 1e-5)
+    gt = gate.to(D).repeat_interleave(T // gates, 0) if gates else torch.ones(1, dtype=D, device=DEV)
+    want = 0.5 * res.to(D) + 2 * gt * u
+    close(out, want, (0.5 * res.to(D)).abs() + (2 * gt * u).abs() + (2 * gt).abs() * mag, "residual")
+    assert (buf[0] == 7).all() and (buf[-1] == 7).all()
+    if pre:
+        n, mag = plain_norm(out, pre, pre_w, None, 1e-5)
+        close(h, n, mag, "h")
+        want_q, want_s = plain_tokens(h)
+        same(q, want_q, "codes")
+        same(q_s, want_s, "scales")
+    res2 = res.clone()  # in place: rows are read ahead of their writing, never behind it
+    hq.hq_residual_norm(y, res2, res2, h=h, post=post, post_w=post_w, gate=gate, alpha=0.5, beta=2.0, pre=pre, pre_w=pre_w,
+                        eps=1e-5)
+    same(res2, out, "in place")

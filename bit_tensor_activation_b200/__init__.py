@@ -26,9 +26,12 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libhq.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is not built: run `python bit_tensor_activation_b200/build.py` "
-                      "(there is no CPU fallback)")
+for _so in (LIB_PATH, os.path.join(_PKG, "_hqargs.so")):
+    if not os.path.exists(_so):
+        raise ImportError(f"{_so} is not built: run `python bit_tensor_activation_b200/build.py` "
+                          "(there is no CPU fallback)")
+
+from . import _hqargs  # noqa: E402
 
 _lib = ctypes.CDLL(LIB_PATH)
 _vp, _i32, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
@@ -123,15 +126,28 @@ def _stream(stream, device):
     return int(stream)
 
 
+class _Dtypes(tuple):
+    """Dtypes an argument may have, and the same as the set that _hqargs takes."""
+
+    def __new__(cls, *dtypes):
+        self = super().__new__(cls, dtypes)
+        self.mask = _hqargs.mask(dtypes)
+        return self
+
+
+_fits = _hqargs.dense  # the address of a contiguous CUDA tensor of the given types and sizes, or None
+
+
 def _ptr(t, dtypes, shape, name):
     if t is None:
         return None
-    if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
-        return t.data_ptr() if t.numel() else None
+    p = _fits(t, -1, dtypes.mask, shape)
+    if p is not None:
+        return p
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
@@ -145,7 +161,7 @@ def _ptr_rows(t, dtypes, shape, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     st = t.stride()
@@ -155,11 +171,13 @@ def _ptr_rows(t, dtypes, shape, name):
     return (t.data_ptr() if t.numel() else None), ld
 
 
-_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
-_F32 = (torch.float32,)
-_I32 = (torch.int32,)
-_U8 = (torch.uint8,)
-_CODES = (torch.int32, torch.uint32)
+_BF16 = _Dtypes(torch.bfloat16, torch.int16, torch.uint16)
+_F32 = _Dtypes(torch.float32)
+_BF16_F32 = _Dtypes(*_BF16, *_F32)
+_I32 = _Dtypes(torch.int32)
+_U8 = _Dtypes(torch.uint8)
+_I8 = _Dtypes(torch.int8)
+_CODES = _Dtypes(torch.int32, torch.uint32)
 
 
 def _check(status, where):
@@ -204,7 +222,7 @@ def _dequant_args(codes, side, keep_idx, rest_idx, scale, zero, out, stream):
     args = (_ptr(codes, _CODES, (P, T, W), "codes"), _ptr(side, _BF16, (P, k, T), "side"), P, T, H, k,
             _ptr(keep_idx, _I32, (k,), "keep_idx"), _ptr(rest_idx, _I32, (H - k,), "rest_idx"),
             _ptr(scale, _F32, (P, H), "scale"), _ptr(zero, _U8, (P, H), "zero"),
-            _ptr(out, _BF16 + _F32, (T, H), "out"), odt, _stream(stream, codes.device))
+            _ptr(out, _BF16_F32, (T, H), "out"), odt, _stream(stream, codes.device))
     return args
 
 
@@ -227,7 +245,7 @@ def hq_compress_reduce(x, keep_idx, rest_idx, scale, inv_scale, zero, out, codes
     args = (_ptr(x, _BF16, (P, T, H), "x"), P, T, H, k, _ptr(keep_idx, _I32, (k,), "keep_idx"),
             _ptr(rest_idx, _I32, (H - k,), "rest_idx"), _ptr(scale, _F32, (P, H), "scale"),
             _ptr(inv_scale, _F32, (P, H), "inv_scale"), _ptr(zero, _U8, (P, H), "zero"),
-            _ptr(out, _BF16 + _F32, (T, H), "out"), odt,
+            _ptr(out, _BF16_F32, (T, H), "out"), odt,
             _ptr(codes, _CODES, (P, T, (H - k) // 8), "codes"), _ptr(side, _BF16, (P, k, T), "side"),
             _stream(stream, x.device))
     _check(_lib.hq_compress_reduce(*args), "hq_compress_reduce")
@@ -248,7 +266,7 @@ def hq_dequant_reduce_ranks(codes, side, keep_idx, rest_idx, scale, zero, out, s
     args = (ctypes.cast(cptr, _vp), ctypes.cast(sptr, _vp) if k else None, P, T, H, k,
             _ptr(keep_idx, _I32, (k,), "keep_idx"), _ptr(rest_idx, _I32, (H - k,), "rest_idx"),
             _ptr(scale, _F32, (P, H), "scale"), _ptr(zero, _U8, (P, H), "zero"),
-            _ptr(out, _BF16 + _F32, (T, H), "out"), odt, _stream(stream, out.device))
+            _ptr(out, _BF16_F32, (T, H), "out"), odt, _stream(stream, out.device))
     _check(_lib.hq_dequant_reduce_ranks(*args), "hq_dequant_reduce_ranks")
 
 
@@ -271,7 +289,7 @@ def hq_two_step_reduce(x, keep_idx, rest_idx, scale, inv_scale, zero, keep2, res
             _ptr(keep2, _I32, (k2,), "keep2"), _ptr(rest2, _I32, (H - k2,), "rest2"),
             _ptr(scale2, _F32, (P, H), "scale2"), _ptr(inv_scale2, _F32, (P, H), "inv_scale2"),
             _ptr(zero2, _U8, (P, H), "zero2"), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _ptr(out, _BF16 + _F32, (T, H), "out"), odt, _stream(stream, x.device))
+            _ptr(out, _BF16_F32, (T, H), "out"), odt, _stream(stream, x.device))
     _check(_lib.hq_two_step_reduce(*args), "hq_two_step_reduce")
 
 
@@ -288,7 +306,7 @@ def hq_two_step_reduce_noalloc(x, keep_idx, rest_idx, scale, inv_scale, zero, ke
             _ptr(inv_scale, _F32, (P, H), "inv_scale"), _ptr(zero, _U8, (P, H), "zero"), k2,
             _ptr(keep2, _I32, (k2,), "keep2"), _ptr(rest2, _I32, (H - k2,), "rest2"),
             _ptr(scale2, _F32, (P, H), "scale2"), _ptr(inv_scale2, _F32, (P, H), "inv_scale2"),
-            _ptr(zero2, _U8, (P, H), "zero2"), _ptr(out, _BF16 + _F32, (T, H), "out"), odt,
+            _ptr(zero2, _U8, (P, H), "zero2"), _ptr(out, _BF16_F32, (T, H), "out"), odt,
             _stream(stream, x.device))
     _check(_lib.hq_two_step_reduce_noalloc(*args), "hq_two_step_reduce_noalloc")
 
@@ -322,7 +340,7 @@ def hq_dequant_reduce_ld(codes, side, keep_idx, rest_idx, scale, zero, out, stre
     if W != (H - k) // 8:
         raise ValueError("codes width does not match the block width and k")
     odt = HQ_OUT_F32 if out.dtype == torch.float32 else HQ_OUT_BF16
-    po, ldo = _ptr_rows(out, _BF16 + _F32, (T, H), "out")
+    po, ldo = _ptr_rows(out, _BF16_F32, (T, H), "out")
     args = (_ptr(codes, _CODES, (P, T, W), "codes"), _ptr(side, _BF16, (P, k, T), "side"), P, T, H, k,
             _ptr(keep_idx, _I32, (k,), "keep_idx"), _ptr(rest_idx, _I32, (H - k,), "rest_idx"),
             _ptr(scale, _F32, (P, H), "scale"), _ptr(zero, _U8, (P, H), "zero"), po, ldo, odt,
@@ -336,7 +354,7 @@ def hq_compress_reduce_ld(x, keep_idx, rest_idx, scale, inv_scale, zero, out, co
     k = keep_idx.shape[0]
     odt = HQ_OUT_F32 if out.dtype == torch.float32 else HQ_OUT_BF16
     px, ldx = _ptr_rows(x, _BF16, (P, T, H), "x")
-    po, ldo = _ptr_rows(out, _BF16 + _F32, (T, H), "out")
+    po, ldo = _ptr_rows(out, _BF16_F32, (T, H), "out")
     args = (px, ldx, P, T, H, k, _ptr(keep_idx, _I32, (k,), "keep_idx"), _ptr(rest_idx, _I32, (H - k,), "rest_idx"),
             _ptr(scale, _F32, (P, H), "scale"), _ptr(inv_scale, _F32, (P, H), "inv_scale"),
             _ptr(zero, _U8, (P, H), "zero"), po, ldo, odt,
@@ -346,18 +364,15 @@ def hq_compress_reduce_ld(x, keep_idx, rest_idx, scale, inv_scale, zero, out, co
 
 
 # -- a row-parallel layer in 8-bit integers around the path --------------------------------------
-_I8 = (torch.int8,)
-
-
 def _dense(t, dev, dtypes, shape, name):
     """Pointer of a contiguous tensor on device `dev`, or None for None: _ptr with the device checked."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    p = _ptr(t, dtypes, shape, name)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} lies on {t.device}, the first tensor on cuda:{dev}")
+    p = _fits(t, dev, dtypes.mask, shape)
+    if p is None:
+        p = _ptr(t, dtypes, shape, name)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} lies on {t.device}, the first tensor on cuda:{dev}")
     return p
 
 
@@ -365,17 +380,17 @@ def _pitched(t, dev, dtypes, shape, multiple, name):
     """(pointer, row pitch in elements) of a tensor [..., n] on device `dev` whose rows are dense and one
     pitch apart.  The strides of dimensions of one element do not count; a tensor of at most one row
     has the pitch of its width rounded up to `multiple`."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
     n = shape[-1]
-    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and n % multiple == 0 and t.is_contiguous():
-        return t.data_ptr(), n
-    if not t.is_cuda:
+    if n % multiple == 0:
+        p = _fits(t, dev, dtypes.mask, shape)
+        if p is not None:
+            return p, n
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} lies on {t.device}, the first tensor on cuda:{dev}")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.numel():
@@ -438,7 +453,7 @@ def hq_int8_matmul(a, a_scale, w, w_scale, out, bias=None, stream=None) -> None:
     H = w.shape[1]
     pa, lda = _pitched(a, dev, _I8, (P, T, K), 16, "a")
     pw, ldw = _pitched(w, dev, _I8, (P, H, K), 16, "w")
-    po, ldo = _pitched(out, dev, _BF16 + _F32, (P, T, H), 8, "out")
+    po, ldo = _pitched(out, dev, _BF16_F32, (P, T, H), 8, "out")
     _call(_lib.hq_int8_matmul, "hq_int8_matmul", dev, stream, pa, lda, _dense(a_scale, dev, _F32, (P, T), "a_scale"), pw,
           ldw, _dense(w_scale, dev, _F32, (P, H), "w_scale"), _dense(bias, dev, _BF16, (P, H), "bias"), P, T, H, K, po,
           ldo, HQ_OUT_F32 if out.dtype == torch.float32 else HQ_OUT_BF16)
@@ -482,9 +497,9 @@ def hq_residual_norm(y, res, res_out, h=None, q=None, q_scale=None, post=HQ_NORM
     if f32 != (res_out.dtype == torch.float32):
         raise TypeError("res and res_out must have the same type")
     pq, ldq = (None, 0) if q is None else _pitched(q, dev, _I8, shape, 16, "q")
-    _call(_lib.hq_residual_norm, "hq_residual_norm", dev, stream, _dense(y, dev, _BF16 + _F32, shape, "y"),
-          HQ_OUT_F32 if y.dtype == torch.float32 else HQ_OUT_BF16, _dense(res, dev, _BF16 + _F32, shape, "res"),
-          _dense(res_out, dev, _BF16 + _F32, shape, "res_out"), HQ_OUT_F32 if f32 else HQ_OUT_BF16, T, H, post,
+    _call(_lib.hq_residual_norm, "hq_residual_norm", dev, stream, _dense(y, dev, _BF16_F32, shape, "y"),
+          HQ_OUT_F32 if y.dtype == torch.float32 else HQ_OUT_BF16, _dense(res, dev, _BF16_F32, shape, "res"),
+          _dense(res_out, dev, _BF16_F32, shape, "res_out"), HQ_OUT_F32 if f32 else HQ_OUT_BF16, T, H, post,
           _dense(post_w, dev, _F32, vector, "post_w"), _dense(post_b, dev, _F32, vector, "post_b"), pg, gate_rows,
           alpha, beta, pre, _dense(pre_w, dev, _F32, vector, "pre_w"), _dense(pre_b, dev, _F32, vector, "pre_b"), eps,
           _dense(h, dev, _BF16, shape, "h"), pq, ldq, _dense(q_scale, dev, _F32, (T,), "q_scale"))

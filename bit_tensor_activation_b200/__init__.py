@@ -126,28 +126,13 @@ def _stream(stream, device):
     return int(stream)
 
 
-class _Dtypes(tuple):
-    """Dtypes an argument may have, and the same as the set that _hqargs takes."""
-
-    def __new__(cls, *dtypes):
-        self = super().__new__(cls, dtypes)
-        self.mask = _hqargs.mask(dtypes)
-        return self
-
-
-_fits = _hqargs.dense  # the address of a contiguous CUDA tensor of the given types and sizes, or None
-
-
 def _ptr(t, dtypes, shape, name):
     if t is None:
         return None
-    p = _fits(t, -1, dtypes.mask, shape)
-    if p is not None:
-        return p
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
@@ -161,7 +146,7 @@ def _ptr_rows(t, dtypes, shape, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     st = t.stride()
@@ -171,18 +156,32 @@ def _ptr_rows(t, dtypes, shape, name):
     return (t.data_ptr() if t.numel() else None), ld
 
 
-_BF16 = _Dtypes(torch.bfloat16, torch.int16, torch.uint16)
-_F32 = _Dtypes(torch.float32)
-_BF16_F32 = _Dtypes(*_BF16, *_F32)
-_I32 = _Dtypes(torch.int32)
-_U8 = _Dtypes(torch.uint8)
-_I8 = _Dtypes(torch.int8)
-_CODES = _Dtypes(torch.int32, torch.uint32)
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_F32 = (torch.float32,)
+_BF16_F32 = _BF16 + _F32
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+_I8 = (torch.int8,)
+_CODES = (torch.int32, torch.uint32)
 
 
 def _check(status, where):
     if status != HQ_OK:
         raise HQError(status, where)
+
+
+def _done(status, where):
+    """Whether _hqargs made the call (whose error is raised here)."""
+    if status is None:
+        return False
+    if status != HQ_OK:
+        raise HQError(status, where)
+    return True
+
+
+def _handle(stream):
+    """A stream argument as _hqargs takes it: None or a number."""
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 def hq_calibrate(x, ema_min, ema_max, beta: float, first_batch: bool, stream=None) -> None:
@@ -227,6 +226,9 @@ def _dequant_args(codes, side, keep_idx, rest_idx, scale, zero, out, stream):
 
 
 def hq_dequant_reduce(codes, side, keep_idx, rest_idx, scale, zero, out, stream=None) -> None:
+    if _done(_hqargs.dequant_reduce(codes, side, keep_idx, rest_idx, scale, zero, out, _handle(stream)),
+             "hq_dequant_reduce"):
+        return
     _check(_lib.hq_dequant_reduce(*_dequant_args(codes, side, keep_idx, rest_idx, scale, zero, out, stream)),
            "hq_dequant_reduce")
 
@@ -364,15 +366,15 @@ def hq_compress_reduce_ld(x, keep_idx, rest_idx, scale, inv_scale, zero, out, co
 
 
 # -- a row-parallel layer in 8-bit integers around the path --------------------------------------
+# Each of these first goes through _hqargs, which looks the arguments over and calls the library; where
+# it says that one does not fit (None), the same checks in Python say which, and how.
 def _dense(t, dev, dtypes, shape, name):
     """Pointer of a contiguous tensor on device `dev`, or None for None: _ptr with the device checked."""
     if t is None:
         return None
-    p = _fits(t, dev, dtypes.mask, shape)
-    if p is None:
-        p = _ptr(t, dtypes, shape, name)
-        if t.get_device() != dev:
-            raise ValueError(f"{name} lies on {t.device}, the first tensor on cuda:{dev}")
+    p = _ptr(t, dtypes, shape, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} lies on {t.device}, the first tensor on cuda:{dev}")
     return p
 
 
@@ -381,16 +383,12 @@ def _pitched(t, dev, dtypes, shape, multiple, name):
     pitch apart.  The strides of dimensions of one element do not count; a tensor of at most one row
     has the pitch of its width rounded up to `multiple`."""
     n = shape[-1]
-    if n % multiple == 0:
-        p = _fits(t, dev, dtypes.mask, shape)
-        if p is not None:
-            return p, n
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} lies on {t.device}, the first tensor on cuda:{dev}")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.numel():
@@ -433,6 +431,8 @@ def _call(fn, where, dev, stream, *args):
 def hq_quantize_tokens(x, q, scale, stream=None) -> None:
     """x [..., K] bf16 to int8 q [..., K] with one scale a row, scale [...] f32; the rows of x and q
     may be further apart than K (multiples of 8 and 16 elements)."""
+    if _done(_hqargs.quantize_tokens(x, q, scale, _handle(stream)), "hq_quantize_tokens"):
+        return
     dev = _device_of(x, "x")
     shape = x.shape
     lead, rows = shape[:-1], 1
@@ -448,6 +448,8 @@ def hq_int8_matmul(a, a_scale, w, w_scale, out, bias=None, stream=None) -> None:
     """Every rank's partial sum out [P, T, H] (bf16 or f32) of int8 activations a [P, T, K] with a
     scale a token (a_scale [P, T]) and int8 weights w [P, H, K] with a scale a channel (w_scale
     [P, H]); bias [P, H] bf16.  The rows of a, w and out may be further apart than K and H."""
+    if _done(_hqargs.int8_matmul(a, a_scale, w, w_scale, out, bias, _handle(stream)), "hq_int8_matmul"):
+        return
     dev = _device_of(a, "a")
     P, T, K = a.shape
     H = w.shape[1]
@@ -464,6 +466,9 @@ def hq_int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, z
     """The wire (codes, side) of the partial sums that hq_int8_matmul would write, bit for bit as
     hq_quantize_pack makes it.  w and w_scale have their rows in the wire's order:
     torch.cat([rest_idx, keep_idx]) of the features' own."""
+    if _done(_hqargs.int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, zero, codes, side,
+                                      _handle(stream)), "hq_int8_matmul_pack"):
+        return
     dev = _device_of(a, "a")
     P, T, K = a.shape
     H = w.shape[1]
@@ -484,6 +489,9 @@ def hq_residual_norm(y, res, res_out, h=None, q=None, q_scale=None, post=HQ_NORM
     int8 with one scale a row (q, q_scale).  y, res, res_out, h [T, H] (y and res bf16 or f32; res_out
     of res's type, res itself allowed); q [T, H] int8, rows may be further apart; weights and biases
     [H] f32; gate [G, H] bf16 with G a divisor of T: row t uses gate row t // (T // G)."""
+    if _done(_hqargs.residual_norm(y, res, res_out, h, q, q_scale, post, post_w, post_b, gate, alpha, beta, pre, pre_w,
+                                   pre_b, eps, _handle(stream)), "hq_residual_norm"):
+        return
     dev = _device_of(y, "y")
     T, H = shape = y.shape
     vector = (H,)

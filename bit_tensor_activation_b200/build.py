@@ -29,16 +29,17 @@ def build(verbose: bool = False, extra_flags=()) -> str:
 
 
 def build_args(verbose: bool = False) -> str:
-    """_hqargs.so: a Python module over torch's own headers and libraries."""
+    """_hqargs.so: a Python module over libhq.so and torch's own headers and libraries."""
     import torch
     from torch.utils import cpp_extension
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    include = [f"-I{p}" for p in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"])]
+    include = [f"-I{p}" for p in (os.path.join(ROOT, "include"), *cpp_extension.include_paths("cuda"),
+                                  sysconfig.get_paths()["include"])]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *include,
-           os.path.join(PKG, "csrc", "hq_args.cpp"), "-o", ARGS_SO, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
-           f"-Wl,-rpath,{lib}"]
+           os.path.join(PKG, "csrc", "hq_args.cpp"), "-o", ARGS_SO, f"-L{PKG}", "-l:libhq.so",
+           f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)

@@ -302,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     const int quad = warp & 3, side = warp >> 2;
     const uint32_t stage = smem_addr(sm.out[warp]);
     MmCols* const cols_of = sm.col[warp];
-    const int Hr = p.H - p.k;
+    const int Hr = p.H - p.k, Wr = Hr >> 3;
     const bool wide = Hr % 32 == 0 && ((uintptr_t)p.codes & 15) == 0;  // a token's words of codes start on 16 bytes
     MmFetch<kOut> next;
     float next_sa = 0.0f;
@@ -335,6 +335,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.acc_full[b], (n >> 1) & 1, abort, lim.consumer))) break;
       tc_fence_after();
       const uint32_t acc = tmem + b * kMmTile + ((uint32_t)(32 * quad) << 16);
+      const bool live = row + lane < p.T;
+      uint32_t* const words =
+          kOut == kMmWire ? p.codes + ((size_t)cur.r * p.T + row + lane) * Wr + (cur.n0 >> 3) : nullptr;
 #pragma unroll 1
       for (int j = first_chunk(n), i = 0; j < kMmChunks; j += kMmSides, ++i) {
         const MmCols& cols = cols_of[i];
@@ -392,19 +395,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           send(n0, w);
           continue;
         }
-        const bool live = row + lane < p.T;
         if (n0 < Hr) {
-          uint32_t words[4];
+          uint32_t x[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) words[q] = wire_word(w + 4 * q, cols, 8 * q);
-          if (live) store_words(p.codes + ((size_t)cur.r * p.T + row + lane) * (Hr / 8) + n0 / 8, words, min(4, (Hr - n0) / 8), wide);
+          for (int q = 0; q < 4; ++q) x[q] = wire_word(w + 4 * q, cols, 8 * q);
+          if (live) store_words(words + 4 * j, x, min(4, (Hr - n0) >> 3), wide);
         }
         if (live && n0 + 32 > Hr) {  // kept features: 32 tokens of one lie beside one another
           uint16_t* s = p.side + ((long long)cur.r * p.k + (n0 - Hr)) * p.T + row + lane;
+          const int c0 = max(Hr - n0, 0), c1 = min(p.H - n0, 32);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const uint32_t x = (w[j / 2] >> (16 * (j & 1))) & 0xFFFFu;
-            if (n0 + j >= Hr && n0 + j < p.H) s[(long long)j * p.T] = (uint16_t)((x & 0x7FFFu) > 0x7F80u ? 0x7FC0u : x);
+          for (int c = 0; c < 32; ++c) {
+            const uint32_t x = (w[c / 2] >> (16 * (c & 1))) & 0xFFFFu;
+            if (c >= c0 && c < c1) s[(long long)c * p.T] = (uint16_t)((x & 0x7FFFu) > 0x7F80u ? 0x7FC0u : x);
           }
         }
       }

@@ -151,6 +151,29 @@ hq::WaitLimits wait_limits() {
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
+// A launch that may begin under the kernel ahead of it in the stream; the kernel waits for that one
+// (grid_wait) before it touches global memory.  cluster > 1: in clusters of that many CTAs.
+template <typename Kernel, typename... Args>
+hq_status launch_dependent(Kernel kern, dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster,
+                           const Args&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return HQ_OK;
+  cudaGetLastError();
+  return HQ_ERR_CUDA;
+}
+
 // One wave of `resident` CTAs over S slices of nb_all row blocks each: every slice gets `base`
 // row chunks and slices 0..extra-1 one more; never more chunks than blocks, at least one.
 struct WaveChunks {
@@ -520,21 +543,17 @@ hq_status quantize_tokens_entry(const uint16_t* x, int ldx, int64_t rows, int K,
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return HQ_ERR_MISALIGNED;
   if (rows == 0) return HQ_OK;
   const RowShape s = row_shape(K);
-  const unsigned grid = (unsigned)(s.warp ? ceil_div(rows, 4) : rows);
+  const dim3 grid((unsigned)(s.warp ? ceil_div(rows, 4) : rows));
+  const long long n = rows;
   cudaStream_t st = (cudaStream_t)stream;
-#define HQ_ROWS(NV, W) hq::quantize_tokens_kernel<NV, W><<<grid, s.threads, 0, st>>>(x, ldx, rows, K, q, ldq, scale)
-  if (s.warp) {
-    if (s.nv == 1) HQ_ROWS(1, true);
-    else if (s.nv == 2) HQ_ROWS(2, true);
-    else HQ_ROWS(4, true);
-  } else {
-    if (s.nv == 1) HQ_ROWS(1, false);
-    else if (s.nv == 2) HQ_ROWS(2, false);
-    else if (s.nv == 4) HQ_ROWS(4, false);
-    else HQ_ROWS(8, false);
-  }
-#undef HQ_ROWS
-  return launched();
+  auto go = [&](auto kern) { return launch_dependent(kern, grid, s.threads, 0, st, 1, x, ldx, n, K, q, ldq, scale); };
+  if (s.warp) return s.nv == 1 ? go(hq::quantize_tokens_kernel<1, true>)
+                  : s.nv == 2  ? go(hq::quantize_tokens_kernel<2, true>)
+                               : go(hq::quantize_tokens_kernel<4, true>);
+  return s.nv == 1   ? go(hq::quantize_tokens_kernel<1, false>)
+         : s.nv == 2 ? go(hq::quantize_tokens_kernel<2, false>)
+         : s.nv == 4 ? go(hq::quantize_tokens_kernel<4, false>)
+                     : go(hq::quantize_tokens_kernel<8, false>);
 }
 
 // The checks that the two products share.
@@ -591,22 +610,8 @@ hq_status launch_few(const hq::MmArgs& p, const CUtensorMap& map_w, DeviceInfo& 
   const int fit = (int)((kSmemPerSm / per_sm - 2560 - 4 * kTokens - red) / hq::few_stage_bytes(kTokens));
   const int stages = std::max(2, std::min({fit, hq::kFewMaxStages, (int)ceil_div(kc, split)}));
   const size_t smem = 1024 + (size_t)stages * hq::few_stage_bytes(kTokens) + red;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(ceil_div(p.H, hq::kFewFeatures) * split), (unsigned)token_tiles, (unsigned)p.P);
-  cfg.blockDim = dim3(hq::kFewThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, map_a, map_w, p, split_log2, stages, wait_limits()) != cudaSuccess) {
-    cudaGetLastError();
-    return HQ_ERR_CUDA;
-  }
-  return HQ_OK;
+  const dim3 grid((unsigned)(ceil_div(p.H, hq::kFewFeatures) * split), (unsigned)token_tiles, (unsigned)p.P);
+  return launch_dependent(kern, grid, hq::kFewThreads, smem, st, split, map_a, map_w, p, split_log2, stages, wait_limits());
 }
 
 template <int kOut>
@@ -632,20 +637,17 @@ hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
   if (raise_smem(d->pair_smem_set[kOut], kern, smem) != HQ_OK) return HQ_ERR_CUDA;
   const long long tiles = (long long)p.P * ceil_div(p.T, hq::kMmTile) * ceil_div(p.H, hq::kMmTile);
   const long long clusters = std::min<long long>(tiles, d->sms / 2);
-  kern<<<(unsigned)(2 * clusters), hq::kMmThreads, smem, st>>>(map_a, map_w, map_out, p, wait_limits());
-  return launched();
+  return launch_dependent(kern, dim3((unsigned)(2 * clusters)), hq::kMmThreads, smem, st, 2, map_a, map_w, map_out, p,
+                          wait_limits());
 }
 
 template <typename Y, typename R>
 hq_status launch_norm(const hq::NormArgs& a, DeviceInfo& d, cudaStream_t st) {
   const RowShape s = row_shape(a.H);
-  if (s.warp) {
-    const unsigned grid = (unsigned)ceil_div(a.T, 4);
-    if (s.nv == 1) hq::residual_norm_kernel<Y, R, 1, 128, true><<<grid, 128, 0, st>>>(a);
-    else if (s.nv == 2) hq::residual_norm_kernel<Y, R, 2, 128, true><<<grid, 128, 0, st>>>(a);
-    else hq::residual_norm_kernel<Y, R, 4, 128, true><<<grid, 128, 0, st>>>(a);
-    return launched();
-  }
+  const dim3 rows((unsigned)a.T), fours((unsigned)ceil_div(a.T, 4));
+  if (s.warp && s.nv == 1) return launch_dependent(hq::residual_norm_kernel<Y, R, 1, 128, true>, fours, 128, 0, st, 1, a);
+  if (s.warp && s.nv == 2) return launch_dependent(hq::residual_norm_kernel<Y, R, 2, 128, true>, fours, 128, 0, st, 1, a);
+  if (s.warp) return launch_dependent(hq::residual_norm_kernel<Y, R, 4, 128, true>, fours, 128, 0, st, 1, a);
   const int nvec = a.H / 8;
   auto threads = [&](int nv) { return (int)(32 * ceil_div(ceil_div(nvec, nv), 32)); };
   // Which kernel, by what was measured (bf16, gate, both weights): the row ring from 4096 < H <= 8192 and
@@ -660,19 +662,15 @@ hq_status launch_norm(const hq::NormArgs& a, DeviceInfo& d, cudaStream_t st) {
     const int stages = (int)std::min<size_t>(hq::kRowsMaxStages, (kSmemPerSm - 2048) / row);
     if (raise_smem(d.norm_smem_set[sizeof(Y) == 4][sizeof(R) == 4][full], kern, kSmemPerSm - 2048) != HQ_OK)
       return HQ_ERR_CUDA;
-    kern<<<(unsigned)d.sms, nt, stages * row, st>>>(a, stages, wait_limits());
-    return launched();
+    return launch_dependent(kern, dim3((unsigned)d.sms), nt, stages * row, st, 1, a, stages, wait_limits());
   }
-  if (nvec > 2 * hq::kRowMaxThreads) {
-    hq::residual_norm_kernel<Y, R, 4, 1024, false><<<a.T, threads(4), 0, st>>>(a);
-  } else if (nvec > hq::kRowMaxThreads) {
-    hq::residual_norm_kernel<Y, R, 4, 512, false><<<a.T, threads(4), 0, st>>>(a);
-  } else if (a.T >= 2 * d.sms) {
-    hq::residual_norm_kernel<Y, R, 2, 512, false><<<a.T, threads(2), 0, st>>>(a);
-  } else {
-    hq::residual_norm_kernel<Y, R, 1, 1024, false><<<a.T, threads(1), 0, st>>>(a);
-  }
-  return launched();
+  if (nvec > 2 * hq::kRowMaxThreads)
+    return launch_dependent(hq::residual_norm_kernel<Y, R, 4, 1024, false>, rows, threads(4), 0, st, 1, a);
+  if (nvec > hq::kRowMaxThreads)
+    return launch_dependent(hq::residual_norm_kernel<Y, R, 4, 512, false>, rows, threads(4), 0, st, 1, a);
+  if (a.T >= 2 * d.sms)
+    return launch_dependent(hq::residual_norm_kernel<Y, R, 2, 512, false>, rows, threads(2), 0, st, 1, a);
+  return launch_dependent(hq::residual_norm_kernel<Y, R, 1, 1024, false>, rows, threads(1), 0, st, 1, a);
 }
 
 // Scratch of hq_two_step_reduce_noalloc: a fixed array in every device's global memory, so that a

@@ -21,6 +21,14 @@ __device__ __forceinline__ void record_error(hq_status s) {
   atomicCAS(&g_error_word, 0u, (unsigned)s);
 }
 
+// A launch that may begin before the kernel ahead of it in the stream is done (programmatic stream
+// serialization): grid_wait() returns once that kernel is complete and its writes are visible, and comes
+// before the first access to global memory; grid_trigger() lets the next such launch begin as soon as
+// every CTA has called it.  It comes after a CTA's allocation of tensor memory: what begins then holds its
+// own only beside CTAs that have theirs.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // bf16 halves of a 32-bit word -> fp32 (exact).
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }

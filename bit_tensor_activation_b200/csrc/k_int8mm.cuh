@@ -207,7 +207,7 @@ __device__ __forceinline__ void store_words(uint32_t* p, const uint32_t* w, int 
 }
 
 template <int kOut>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
+__global__ void __launch_bounds__(kMmThreads, 1)
     int8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                             const __grid_constant__ CUtensorMap map_out, const MmArgs p, WaitLimits lim) {
   extern __shared__ unsigned char s_raw[];
@@ -239,6 +239,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  grid_trigger();
+  grid_wait();
 
   if (warp == kMmEpiWarps) {  // ---------------------------------------------- loads
     if (lane == 0) {
@@ -561,6 +563,11 @@ __global__ void __launch_bounds__(kFewThreads)
   if (split > 1) cluster_arrive();  // here: this CTA's memory may be written
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  grid_trigger();
+  // the weights start on their way into L2 under the kernel that makes the activations (whatever it writes
+  // goes through L2 as well, so this brings nothing stale)
+  if (warp == 4 && lane < c1 - c0) tma_prefetch_3d(&map_w, (c0 + lane) * kMmK, n0, r);
+  grid_wait();
 
   if (warp == 4) {  // ---------------------------------------------------------- loads
     if (lane == 0) {

@@ -172,6 +172,8 @@ __device__ __forceinline__ void store_row(RowGroup<kWarpRow>& g, const NormArgs&
 template <typename Y, typename R, int NV, int kMaxThreads, bool kWarpRow>
 __global__ void __launch_bounds__(kMaxThreads) residual_norm_kernel(const NormArgs a) {
   __shared__ float s_red[2 * kRowMaxWarps];
+  grid_trigger();
+  grid_wait();
   RowGroup<kWarpRow> g{s_red, 0};
   const int i = kWarpRow ? (threadIdx.x & 31) : threadIdx.x;
   const int nt = kWarpRow ? 32 : blockDim.x;
@@ -270,6 +272,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) residual_norm_rows_kernel(con
     fence_barrier_init();
   }
   __syncthreads();
+  grid_trigger();
+  grid_wait();
   // thread 0 loads row `row` into stage s
   auto load = [&](int row, int s) {
     mbar_arrive_expect_tx(&s_full[s], stage_bytes);

@@ -14,6 +14,8 @@ __global__ void __launch_bounds__(kWarpRow ? 128 : kRowMaxThreads)
     quantize_tokens_kernel(const uint16_t* __restrict__ x, int ldx, long long rows, int K, int8_t* __restrict__ q,
                            int ldq, float* __restrict__ scale) {
   __shared__ float s_red[2 * kRowMaxWarps];
+  grid_trigger();
+  grid_wait();
   RowGroup<kWarpRow> g{s_red, 0};
   const int i = kWarpRow ? (threadIdx.x & 31) : threadIdx.x;
   const int nt = kWarpRow ? 32 : blockDim.x;

@@ -58,7 +58,7 @@ struct DeviceInfo {
   bool select_smem_set = false;
   bool pair_smem_set[3] = {};        // [output]
   bool norm_smem_set[2][2][2] = {};  // [fp32 y][fp32 residual][threads all full]
-  bool few_smem_set[3][4] = {};      // [output][tokens 16, 32, 64, 128]
+  bool few_smem_set[3][3] = {};      // [output][tokens 16, 32, 64]
   OccupancyCache dequant_tma[2][2];  // [fp32 out][bf16 shards]
   OccupancyCache dequant_cp[2][2];
   OccupancyCache fused[2];           // [fp32 out]
@@ -597,14 +597,17 @@ hq_status launch_few(const hq::MmArgs& p, const CUtensorMap& map_w, DeviceInfo& 
   CUtensorMap map_a;
   if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, kTokens, 128)) return HQ_ERR_CUDA;
   auto kern = hq::int8_matmul_few_kernel<kOut, kTokens>;
-  constexpr int kIdx = kTokens == 16 ? 0 : kTokens == 32 ? 1 : kTokens == 64 ? 2 : 3;
+  constexpr int kIdx = kTokens == 16 ? 0 : kTokens == 32 ? 1 : 2;
   if (raise_smem(d.few_smem_set[kOut][kIdx], kern, kSmemPerSm - 1024) != HQ_OK) return HQ_ERR_CUDA;
-  // K is shared by a cluster until the CTAs are about two to an SM (and none is left without a step);
-  // the ring of an SM's CTAs together fills its shared memory.
+  // K is shared by a cluster of CTAs until they are one to an SM, or two with at least eight steps each
+  // (4 ranks, 32 tokens, H = 4096, K = 1024 as a wire: 6.4 us with 128 CTAs, 7.1 with 256 of four steps;
+  // 64 tokens, 8192 x 8192: 18.2 us with 128 CTAs, 16.2 with 256).  An SM's CTAs fill its shared memory
+  // with their rings together (8 ranks, one token, H = 8192, K = 1024: four to an SM 12.1 us, three 15.0).
   const int kc = (int)ceil_div(p.K, hq::kMmK);
   const long long token_tiles = ceil_div(p.T, kTokens), tiles = ceil_div(p.H, hq::kFewFeatures) * token_tiles * p.P;
   int split = 1, split_log2 = 0;
-  while (split < hq::kFewMaxSplit && 2 * split <= kc && 2 * split * tiles <= 2 * d.sms) split *= 2, ++split_log2;
+  auto fits = [&](int s) { return s <= kc && (s * tiles <= d.sms || (s * tiles <= 2 * d.sms && kc / s >= 8)); };
+  while (split < hq::kFewMaxSplit && fits(2 * split)) split *= 2, ++split_log2;
   const size_t red = split > 1 ? hq::few_red_bytes(kTokens) : 0;
   const int per_sm = (int)std::min<long long>(4, std::max<long long>(1, ceil_div(tiles * split, d.sms)));
   const int fit = (int)((kSmemPerSm / per_sm - 2560 - 4 * kTokens - red) / hq::few_stage_bytes(kTokens));
@@ -620,10 +623,13 @@ hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
   if (device_info(&d) != HQ_OK) return HQ_ERR_CUDA;
   CUtensorMap map_a, map_w, map_out;
   if (!encode_3d(&map_w, p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.H, p.P, p.ldw, hq::kMmHalf, 128)) return HQ_ERR_CUDA;
+  // Up to 64 tokens the weights are the M operand: 8 ranks, H = 8192, K = 1024 take 13.3 us at 32 tokens
+  // and 15.0 at 64 (the pair kernel: 16.7 and 17.0); 8192 x 8192 with one rank, 40 tokens 16.1 and 24.3.
+  // Beyond, the pair kernel's tiles are the faster ones: 65 tokens 17.0 us (23.2 with the weights as M
+  // and room for 128 tokens), 128 tokens 17.8 and 26.2; as a wire 21.4 and 41.1.
   if (p.T <= 16) return launch_few<kOut, 16>(p, map_w, *d, st);
   if (p.T <= 32) return launch_few<kOut, 32>(p, map_w, *d, st);
   if (p.T <= 64) return launch_few<kOut, 64>(p, map_w, *d, st);
-  if (p.T <= 128) return launch_few<kOut, 128>(p, map_w, *d, st);
   if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, hq::kMmHalf, 128)) return HQ_ERR_CUDA;
   memset(&map_out, 0, sizeof map_out);
   if (kOut == hq::kMmBf16 &&

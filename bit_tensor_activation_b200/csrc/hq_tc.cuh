@@ -167,4 +167,12 @@ __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float4 ld_shared_float4(uint32_t addr) {  // 4-byte aligned
+  float4 v;
+  asm volatile("ld.shared.f32 %0, [%4];\n\tld.shared.f32 %1, [%4+4];\n\tld.shared.f32 %2, [%4+8];\n\tld.shared.f32 %3, [%4+12];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
 }  // namespace hq

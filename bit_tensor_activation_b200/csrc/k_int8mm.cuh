@@ -341,17 +341,17 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       uint32_t* const words =
           kOut == kMmWire ? p.codes + ((size_t)cur.r * p.T + row + lane) * Wr + (cur.n0 >> 3) : nullptr;
 #pragma unroll 1
-      for (int j = first_chunk(n), i = 0; j < kMmChunks; j += kMmSides, ++i) {
+      for (int chunk = first_chunk(n), i = 0; chunk < kMmChunks; chunk += kMmSides, ++i) {
         const MmCols& cols = cols_of[i];
         uint32_t v[32];
-        tc_load(acc + 32 * j, v);
-        if (j + kMmSides >= kMmChunks) {  // the warp's last read of the tile: its columns may be written again
+        tc_load(acc + 32 * chunk, v);
+        if (chunk + kMmSides >= kMmChunks) {  // the warp's last read of the tile: its columns may be written again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&sm.acc_empty[b]), 0));
         }
         if (kOut == kMmWire && i == 1 && more) next.grids(p, at.r, at.n0, first_chunk(n + 1), lane);
-        const int n0 = cur.n0 + 32 * j;
+        const int n0 = cur.n0 + 32 * chunk;
         if (n0 >= p.H || row >= p.T) continue;
         float f[32];
 #pragma unroll
@@ -381,35 +381,32 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           __syncwarp();
           if (lane == 0) tma_store_3d(&map_out, stage, at_col, row, cur.r);
         };
-        if (kOut == kMmF32) {
+        if constexpr (kOut == kMmF32) {
           uint32_t x[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(f[j]);
           send(n0, x);
           if (n0 + 16 < p.H) send(n0 + 16, x + 16);
-          continue;
-        }
-        uint32_t w[16];
+        } else {
+          uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          w[j] = kOut == kMmBf16 ? pack_bf16x2(f[2 * j], f[2 * j + 1]) : round_bf16x2(f[2 * j], f[2 * j + 1]);
-        if (kOut == kMmBf16) {
-          send(n0, w);
-          continue;
-        }
-        if (n0 < Hr) {
-          uint32_t x[4];
+          for (int j = 0; j < 16; ++j)
+            w[j] = kOut == kMmBf16 ? pack_bf16x2(f[2 * j], f[2 * j + 1]) : round_bf16x2(f[2 * j], f[2 * j + 1]);
+          if (kOut == kMmBf16) send(n0, w);
+          if (kOut == kMmWire && n0 < Hr) {
+            uint32_t x[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) x[q] = wire_word(w + 4 * q, cols, 8 * q);
-          if (live) store_words(words + 4 * j, x, min(4, (Hr - n0) >> 3), wide);
-        }
-        if (live && n0 + 32 > Hr) {  // kept features: 32 tokens of one lie beside one another
-          uint16_t* s = p.side + ((long long)cur.r * p.k + (n0 - Hr)) * p.T + row + lane;
-          const int c0 = max(Hr - n0, 0), c1 = min(p.H - n0, 32);
+            for (int q = 0; q < 4; ++q) x[q] = wire_word(w + 4 * q, cols, 8 * q);
+            if (live) store_words(words + 4 * chunk, x, min(4, (Hr - n0) >> 3), wide);
+          }
+          if (kOut == kMmWire && live && n0 + 32 > Hr) {  // kept features: 32 tokens of one lie beside one another
+            uint16_t* s = p.side + (size_t)cur.r * p.k * p.T + row + lane;
+            const int c0 = max(Hr - n0, 0), c1 = min(p.H - n0, 32);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const uint32_t x = (w[c / 2] >> (16 * (c & 1))) & 0xFFFFu;
-            if (c >= c0 && c < c1) s[(long long)c * p.T] = (uint16_t)((x & 0x7FFFu) > 0x7F80u ? 0x7FC0u : x);
+            for (int c = 0; c < 32; ++c) {
+              const uint32_t x = (w[c / 2] >> (16 * (c & 1))) & 0xFFFFu;
+              if (c >= c0 && c < c1) s[(size_t)(n0 + c - Hr) * p.T] = (uint16_t)((x & 0x7FFFu) > 0x7F80u ? 0x7FC0u : x);
+            }
           }
         }
       }
@@ -464,22 +461,31 @@ struct FewFeature {
     }
   }
 
-  // `count` (at most 8) tokens from t on, whose sums are acc and whose scales lie at sa.  All lanes of a
-  // warp hold neighbouring features and call together.
-  __device__ __forceinline__ void emit(const uint32_t (&acc)[8], int t, int count, const float* sa) {
+  // `count` (at most N) tokens from t on, whose sums are acc and whose scales lie at sa.  All lanes of a
+  // warp hold neighbouring features and call together.  The values are independent of one another: with 32
+  // at a time the latencies of a conversion, a shuffle and a store are those of one, not of four groups.
+  template <int N>
+  __device__ __forceinline__ void emit(const uint32_t (&acc)[N], int t, int count, uint32_t sa) {
     const int lane = threadIdx.x & 31, Hr = p.H - p.k;
     count = min(count, p.T - t);
     if (count <= 0) return;
-    float v[8];
+    float v[N];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = __fmul_rn(__fmul_rn(__int2float_rn((int)acc[j]), j < count ? sa[j] : 0.0f), scale);
-      if (kOut != kMmWire && p.bias) v[j] = __fadd_rn(v[j], second);
+    for (int j = 0; j < N; j += 4) {
+      const float4 s = ld_shared_float4(sa + 4 * j);
+      fmul2(v[j], v[j + 1], __int2float_rn((int)acc[j]), __int2float_rn((int)acc[j + 1]), s.x, s.y);
+      fmul2(v[j + 2], v[j + 3], __int2float_rn((int)acc[j + 2]), __int2float_rn((int)acc[j + 3]), s.z, s.w);
+      fmul2(v[j], v[j + 1], v[j], v[j + 1], scale, scale);
+      fmul2(v[j + 2], v[j + 3], v[j + 2], v[j + 3], scale, scale);
+    }
+    if (kOut != kMmWire && p.bias) {
+#pragma unroll
+      for (int j = 0; j < N; j += 2) fadd2(v[j], v[j + 1], v[j], v[j + 1], second, second);
     }
     if (kOut == kMmF32) {
       float* o = static_cast<float*>(p.out) + ((size_t)r * p.T + t) * p.ldo + n;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < N; ++j)
         if (on && j < count) o[(size_t)j * p.ldo] = v[j];
     } else if (kOut == kMmBf16) {
       // two tokens at a time: an even lane takes the first token's features n, n + 1, an odd lane the
@@ -487,7 +493,7 @@ struct FewFeature {
       const bool odd = lane & 1;
       uint16_t* o = static_cast<uint16_t*>(p.out) + ((size_t)r * p.T + t + odd) * p.ldo + (n - odd);
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
+      for (int j = 0; j < N; j += 2) {
         const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
         const uint32_t w = odd ? pack_bf16x2(other, v[j + 1]) : pack_bf16x2(v[j], other);
         if (on && j + odd < count) *reinterpret_cast<uint32_t*>(o + (size_t)j * p.ldo) = w;
@@ -496,27 +502,30 @@ struct FewFeature {
       // a token's code of this feature to nibble lane % 8, then 8 tokens x 8 lanes are exchanged so that
       // lane i of 8 holds the whole word of token t + i
       const int i = lane & 7;
-      uint32_t x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float b = bf16_lo(round_bf16x2(v[j], 0.0f));
-        const int c = __float2int_rn(__fmul_rn(b, second));  // saturating; NaN -> 0
-        x[j] = (uint32_t)(min(max(c, -zero), 15 - zero) + zero) << (4 * i);
-      }
+      for (int j0 = 0; j0 < N; j0 += 8) {
+        uint32_t x[8];
 #pragma unroll
-      for (int step = 0; step < 3; ++step) {
-        const bool up = (i >> step) & 1;
-#pragma unroll
-        for (int j = 0; j < (4 >> step); ++j) {
-          const uint32_t keep = up ? x[2 * j + 1] : x[2 * j], give = up ? x[2 * j] : x[2 * j + 1];
-          x[j] = keep | __shfl_xor_sync(0xFFFFFFFFu, give, 1 << step);
+        for (int j = 0; j < 8; ++j) {
+          const float b = bf16_lo(round_bf16x2(v[j0 + j], 0.0f));
+          const int c = __float2int_rn(__fmul_rn(b, second));  // saturating; NaN -> 0
+          x[j] = (uint32_t)(min(max(c, -zero), 15 - zero) + zero) << (4 * i);
         }
+#pragma unroll
+        for (int step = 0; step < 3; ++step) {
+          const bool up = (i >> step) & 1;
+#pragma unroll
+          for (int j = 0; j < (4 >> step); ++j) {
+            const uint32_t keep = up ? x[2 * j + 1] : x[2 * j], give = up ? x[2 * j] : x[2 * j + 1];
+            x[j] = keep | __shfl_xor_sync(0xFFFFFFFFu, give, 1 << step);
+          }
+        }
+        if (n < Hr && j0 + i < count) p.codes[((size_t)r * p.T + t + j0 + i) * (Hr / 8) + (n >> 3)] = x[0];
       }
-      if (n < Hr && i < count) p.codes[((size_t)r * p.T + t + i) * (Hr / 8) + (n >> 3)] = x[0];
       if (on && n >= Hr) {
         uint16_t* s = p.side + ((size_t)r * p.k + (n - Hr)) * p.T + t;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < N; ++j)
           if (j < count) s[j] = (uint16_t)pack_bf16x2(v[j], 0.0f);
       }
     }
@@ -529,7 +538,7 @@ __global__ void __launch_bounds__(kFewThreads)
                            const MmArgs p, int split_log2, int stages, WaitLimits lim) {
   extern __shared__ unsigned char s_raw[];
   __shared__ uint64_t s_full[kFewMaxStages], s_empty[kFewMaxStages], s_acc;
-  __shared__ float s_scale[kTokens];
+  __shared__ __align__(16) float s_scale[kTokens + 32];  // the last group's loads may go past the tokens
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   unsigned char* const base =
@@ -617,15 +626,16 @@ __global__ void __launch_bounds__(kFewThreads)
     ok = __all_sync(0xFFFFFFFFu, ok);
     tc_fence_after();
     if (ok && split == 1) {
+      constexpr int kGroup = kTokens < 32 ? 8 : 32;
 #pragma unroll 1
-      for (int j = 0; j < kTokens; j += 8) {
-        uint32_t v[8];
+      for (int j = 0; j < kTokens && t0 + j < p.T; j += kGroup) {
+        uint32_t v[kGroup];
         tc_load(acc + j, v);
-        feature.emit(v, t0 + j, 8, s_scale + j);
+        feature.emit(v, t0 + j, kGroup, smem_addr(s_scale + j));
       }
     } else if (ok) {
       // the columns go to the CTAs that add them up
-      constexpr int kTokensLog2 = kTokens == 16 ? 4 : kTokens == 32 ? 5 : kTokens == 64 ? 6 : 7;
+      constexpr int kTokensLog2 = kTokens == 16 ? 4 : kTokens == 32 ? 5 : 6;
       const int width_log2 = kTokensLog2 - split_log2;
       const uint32_t mine = smem_addr(red + ((rank << width_log2) * kFewFeatures + threadIdx.x));
 #pragma unroll 1
@@ -659,7 +669,7 @@ __global__ void __launch_bounds__(kFewThreads)
           for (int i = 0; i < 8; ++i)
             if (c + i < width) v[i] += ld_shared(at + 4 * i * kFewFeatures);
         }
-        feature.emit(v, t0 + rank * width + c, width - c, s_scale + rank * width + c);
+        feature.emit(v, t0 + rank * width + c, min(width - c, 8), smem_addr(s_scale) + 4 * (rank * width + c));
       }
     }
   }

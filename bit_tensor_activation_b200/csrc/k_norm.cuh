@@ -275,7 +275,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) residual_norm_rows_kernel(con
   grid_trigger();
   grid_wait();
   // thread 0 loads row `row` into stage s
+  int issued = 0;
   auto load = [&](int row, int s) {
+    ++issued;
     mbar_arrive_expect_tx(&s_full[s], stage_bytes);
     bulk_load(ring + s * stage_bytes, static_cast<const Y*>(a.y) + (size_t)row * H, y_bytes, &s_full[s]);
     bulk_load(ring + s * stage_bytes + y_bytes, static_cast<const R*>(a.res) + (size_t)row * H, r_bytes, &s_full[s]);
@@ -342,7 +344,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) residual_norm_rows_kernel(con
   }
   if (i == 0 && *abort) {  // the copies in flight have landed before the CTA leaves
     int ignore = 0;
-    for (int q = 0; q < stages; ++q) mbar_wait(&s_full[q], 0, &ignore, lim.producer);
+    for (int q = max(0, issued - stages); q < issued; ++q)
+      mbar_wait(&s_full[q % stages], (q / stages) & 1, &ignore, lim.producer);
   }
 }
 

@@ -37,7 +37,8 @@ from dataclasses import dataclass
 import torch
 import torch.distributed as dist
 
-from . import (hq_calibrate, hq_dequant_reduce, hq_dequant_reduce_ranks, hq_quantize_pack, hq_select_topk)
+from . import (HQ_NORM_NONE, HQ_NORM_RMS, hq_calibrate, hq_dequant_reduce, hq_dequant_reduce_ranks,
+               hq_int8_matmul_pack, hq_quantize_pack, hq_quantize_tokens, hq_residual_norm, hq_select_topk)
 
 
 # ---------------------------------------------------------------------------------------------
@@ -181,6 +182,19 @@ class HybridAllReduce:
         hq_quantize_pack(xin, p.keep_idx, p.rest_idx, self.inv, self.zero, self.codes, self.side, stream=stream)
         return self.codes, self.side
 
+    def pack_product(self, a: torch.Tensor, a_scale: torch.Tensor, weights: "WireWeights", stream=None):
+        """pack of the partial sum a [T, K] int8 (a_scale [T]) times this rank's weights, with no partial
+        sum in memory: the wire, bit for bit, of pack(hq_int8_matmul(...))."""
+        p, P = self.p, self.p.P
+        blocks = 1 if self.scheme == "allgather" else P  # a call a row block: all of them take the same weights
+        rows = self.T // blocks
+        for j in range(blocks):
+            t = slice(j * rows, (j + 1) * rows)
+            hq_int8_matmul_pack(a[None, t], a_scale[None, t], weights.w, weights.scale, p.keep_idx, p.rest_idx,
+                                self.inv[j:j + 1], self.zero[j:j + 1], self.codes[j:j + 1], self.side[j:j + 1],
+                                stream=stream)
+        return self.codes, self.side
+
     def exchange(self, codes: torch.Tensor, side: torch.Tensor):
         if self.scheme == "allgather":
             return allgather_stack(codes, self.group), allgather_stack(side, self.group)
@@ -239,6 +253,14 @@ class PeerAllReduce:
         hq_quantize_pack(x.unsqueeze(0), p.keep_idx, p.rest_idx, self.inv, self.zero, codes.unsqueeze(0),
                          side.unsqueeze(0), stream=stream)
 
+    def pack_product(self, a: torch.Tensor, a_scale: torch.Tensor, weights: "WireWeights", stream=None) -> None:
+        """pack of the partial sum a [T, K] int8 (a_scale [T]) times this rank's weights, straight into this
+        rank's wire."""
+        p = self.p
+        codes, side = self.wires[self.rank]
+        hq_int8_matmul_pack(a[None], a_scale[None], weights.w, weights.scale, p.keep_idx, p.rest_idx, self.inv, self.zero,
+                            codes.unsqueeze(0), side.unsqueeze(0), stream=stream)
+
     def reduce(self, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         p = self.p
         if out is None:
@@ -253,6 +275,69 @@ class PeerAllReduce:
         out = self.reduce(out)
         self.barrier()   # every rank has read the wires
         return out
+
+
+# ---------------------------------------------------------------------------------------------
+# A row-parallel layer in 8-bit integers around the compressed sum
+# ---------------------------------------------------------------------------------------------
+@dataclass
+class WireWeights:
+    """A rank's int8 weights with their rows in the wire's order: w [1, H, K], scale [1, H] (a scale a
+    feature).  Laid out once, after the selection; rows are padded to a multiple of 16 bytes."""
+
+    w: torch.Tensor
+    scale: torch.Tensor
+
+    @classmethod
+    def lay_out(cls, w: torch.Tensor, scale: torch.Tensor, params: HybridParams) -> "WireWeights":
+        """From this rank's weights w [H, K] int8 and scale [H] in the features' own order."""
+        order = torch.cat([params.rest_idx, params.keep_idx]).long()
+        H, K = w.shape
+        rows = torch.zeros((1, H, -(-K // 16) * 16), dtype=torch.int8, device=w.device)
+        rows[0, :, :K] = w[order]
+        return cls(rows[..., :K], scale[order].unsqueeze(0).contiguous())
+
+
+class Int8RowParallel:
+    """This rank's part of a row-parallel layer, from its activations to the end of the block.
+
+    ``wire(x)`` quantizes the activations x [T, K] bf16 token by token and writes the product's wire;
+    the reducer (``HybridAllReduce`` or ``PeerAllReduce``) exchanges and sums it; ``finish`` adds the sum,
+    normed and gated, to the residual and norms that for the next layer, whose int8 product takes q and
+    q_scale as they are."""
+
+    def __init__(self, reducer, w: torch.Tensor, w_scale: torch.Tensor):
+        self.reducer = reducer
+        self.weights = WireWeights.lay_out(w, w_scale, reducer.p)
+        T, K = reducer.T, w.shape[1]
+        self.a = torch.empty((T, -(-K // 16) * 16), dtype=torch.int8, device=w.device)[:, :K]
+        self.a_scale = torch.empty((T,), dtype=torch.float32, device=w.device)
+        H = reducer.p.H
+        self.q = torch.empty((T, -(-H // 16) * 16), dtype=torch.int8, device=w.device)[:, :H]
+        self.q_scale = torch.empty((T,), dtype=torch.float32, device=w.device)
+
+    def wire(self, x: torch.Tensor, stream=None):
+        hq_quantize_tokens(x, self.a, self.a_scale, stream=stream)
+        return self.reducer.pack_product(self.a, self.a_scale, self.weights, stream=stream)
+
+    def finish(self, total: torch.Tensor, res: torch.Tensor, post: int = HQ_NORM_NONE, post_w=None, gate=None,
+               alpha: float = 1.0, beta: float = 1.0, pre: int = HQ_NORM_RMS, pre_w=None, eps: float = 1e-6,
+               stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+        """The new residual goes into res; returns the next product's (q [T, H], q_scale [T])."""
+        hq_residual_norm(total, res, res, q=self.q, q_scale=self.q_scale, post=post, post_w=post_w, gate=gate, alpha=alpha,
+                         beta=beta, pre=pre, pre_w=pre_w, eps=eps, stream=stream)
+        return self.q, self.q_scale
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        """The ranks' sum [T, H] of the layer."""
+        r = self.reducer
+        wire = self.wire(x)
+        if isinstance(r, PeerAllReduce):
+            r.barrier()
+            out = r.reduce(out)
+            r.barrier()
+            return out
+        return r.reduce(*r.exchange(*wire), out=out)
 
 
 def symmetric_wires(params: HybridParams, T: int, group=None, timeout_ms: int = 10000):

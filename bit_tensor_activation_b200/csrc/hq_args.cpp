@@ -125,18 +125,24 @@ struct Args {
   }
 };
 
-// The library's call on the arguments' device; a C++ exception becomes "does not fit".
+// The library's call on the arguments' device.
 template <typename Call>
 PyObject* run(Args& a, Call call) {
   if (!a.ok) Py_RETURN_NONE;
-  int status;
+  const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(a.dev)));
+  return PyLong_FromLong(call());
+}
+
+// A method as Python calls it.  A tensor without storage or with symbolic sizes throws when it is asked for
+// them: such a one does not fit.
+template <PyObject* (*kMethod)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* caught(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   try {
-    const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(a.dev)));
-    status = call();
+    return kMethod(self, args, n);
   } catch (...) {
+    PyErr_Clear();
     Py_RETURN_NONE;
   }
-  return PyLong_FromLong(status);
 }
 
 // quantize_tokens(x, q, scale, stream)
@@ -262,7 +268,8 @@ PyObject* residual_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-#define HQ_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
+#define HQ_METHOD(name) \
+  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(caught<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {HQ_METHOD(quantize_tokens), HQ_METHOD(int8_matmul),   HQ_METHOD(int8_matmul_pack),
                          HQ_METHOD(dequant_reduce),  HQ_METHOD(residual_norm), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hqargs", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
       }
     }
-    if (kOut != kMmWire && lane == 0) tma_store_wait_read<0>();
+    if (kOut != kMmWire && lane == 0) tma_store_wait();
   }
   __syncwarp();
   tc_fence_before();

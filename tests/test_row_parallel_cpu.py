@@ -80,6 +80,21 @@ def test_the_binding_refuses_tensors_of_the_host():
         hq.hq_residual_norm(x, x, x, h=x)
 
 
+def test_tensors_without_storage_are_refused_not_fatal():
+    """A fake tensor throws in C++ when it is asked for its address; the binding says what is wrong."""
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    with FakeTensorMode():
+        x, q, s = (torch.empty(4, 64, dtype=torch.bfloat16), torch.empty(4, 64, dtype=torch.int8), torch.empty(4))
+        with pytest.raises(TypeError):
+            hq.hq_quantize_tokens(x, q, s)
+    with pytest.raises(TypeError):
+        hq.hq_int8_matmul(None, None, None, None, None)
+    with pytest.raises((TypeError, AttributeError)):
+        hq.hq_residual_norm(torch.zeros(4, 64, dtype=torch.bfloat16, device="meta"), None, None)
+
+
 def half_even(f: Fraction) -> int:
     return round(f)  # Python rounds a Fraction's half to even
 

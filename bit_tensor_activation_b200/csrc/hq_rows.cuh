@@ -99,9 +99,9 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
 // Vector j (elements 8j .. 8j+7) of a bf16 row of n elements; what lies at or beyond n reads as 0
 // and is not touched in memory.
 __device__ __forceinline__ uint4 load_row8(const uint16_t* __restrict__ row, int j, int n) {
-  if (8 * j + 8 <= n) return ld_stream16(row + 8 * j);
+  if (8 * j + 8 <= n) return ld_dep_stream16(row + 8 * j);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
-  for (int i = 0; 8 * j + i < n; ++i) w[i >> 1] |= (uint32_t)row[8 * j + i] << (16 * (i & 1));
+  for (int i = 0; 8 * j + i < n; ++i) w[i >> 1] |= ld_dep(row + 8 * j + i) << (16 * (i & 1));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void store_codes8(int8_t* __restrict__ row, int j, int n, uint2 c) {

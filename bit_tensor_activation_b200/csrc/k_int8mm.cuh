@@ -169,9 +169,9 @@ struct MmFetch {
       const int c = column(n0, j0, i, lane);
       const size_t g = (size_t)r * p.H + c;
       const bool on = j0 + kMmSides * i < kMmChunks && c < p.H;
-      scale[i] = on ? __ldg(p.w_scale + g) : 0.0f;
-      second[i] = kOut != kMmWire && p.bias && on ? bf16_lo(__ldg(p.bias + g)) : 0.0f;
-      rest[i] = kOut == kMmWire && on && c < p.H - p.k ? __ldg(p.rest_idx + c) : 0;
+      scale[i] = on ? ld_dep(p.w_scale + g) : 0.0f;
+      second[i] = kOut != kMmWire && p.bias && on ? bf16_lo(ld_dep(p.bias + g)) : 0.0f;
+      rest[i] = kOut == kMmWire && on && c < p.H - p.k ? ld_dep(p.rest_idx + c) : 0;
       zero[i] = 0;
     }
   }
@@ -181,8 +181,8 @@ struct MmFetch {
     for (int i = 0; i < kMmWarpChunks; ++i) {
       if (j0 + kMmSides * i >= kMmChunks || column(n0, j0, i, lane) >= p.H - p.k) continue;
       const size_t g = (size_t)r * p.H + checked_index(rest[i], p.H);
-      second[i] = __ldg(p.inv_scale + g);
-      zero[i] = __ldg(p.zero + g);
+      second[i] = ld_dep(p.inv_scale + g);
+      zero[i] = ld_dep(p.zero + g);
     }
   }
   __device__ __forceinline__ void store(MmCols* s, int lane) const {
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     auto first_chunk = [&](int n) { return (side + (kMmSides - kMmChunks % kMmSides) * n) % kMmSides; };
     auto fetch = [&](const MmTileAt& at, int n) {
       const int row = at.t0 + (int)cta * kMmHalf + 32 * quad + lane;
-      next_sa = row < p.T ? __ldg(p.a_scale + (size_t)at.r * p.T + row) : 0.0f;
+      next_sa = row < p.T ? ld_dep(p.a_scale + (size_t)at.r * p.T + row) : 0.0f;
       next.start(p, at.r, at.n0, first_chunk(n), lane);
     };
     int n = 0;
@@ -452,12 +452,12 @@ struct FewFeature {
   __device__ __forceinline__ FewFeature(const MmArgs& p, int r, int n) : p(p), r(r), n(n), on(n < p.H) {
     if (!on) return;
     const size_t g = (size_t)r * p.H + n;
-    scale = __ldg(p.w_scale + g);
-    if (kOut != kMmWire && p.bias) second = bf16_lo(__ldg(p.bias + g));
+    scale = ld_dep(p.w_scale + g);
+    if (kOut != kMmWire && p.bias) second = bf16_lo(ld_dep(p.bias + g));
     if (kOut == kMmWire && n < p.H - p.k) {
-      const size_t h = (size_t)r * p.H + checked_col(p.rest_idx, n, p.H);
-      second = __ldg(p.inv_scale + h);
-      zero = __ldg(p.zero + h);
+      const size_t h = (size_t)r * p.H + checked_index(ld_dep(p.rest_idx + n), p.H);
+      second = ld_dep(p.inv_scale + h);
+      zero = ld_dep(p.zero + h);
     }
   }
 
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kFewThreads)
   bool ok = true;
   if (warp < 4) {  // ------------------------------------------------------------ epilogue
     for (int j = threadIdx.x; j < kTokens; j += 128)
-      s_scale[j] = t0 + j < p.T ? __ldg(p.a_scale + (size_t)r * p.T + t0 + j) : 0.0f;
+      s_scale[j] = t0 + j < p.T ? ld_dep(p.a_scale + (size_t)r * p.T + t0 + j) : 0.0f;
     named_barrier_sync(128);
     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_acc, 0, abort, lim.consumer)) && !*abort;
     ok = __all_sync(0xFFFFFFFFu, ok);

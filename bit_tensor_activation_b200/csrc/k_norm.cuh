@@ -42,7 +42,7 @@ struct Raw8 {
   __device__ __forceinline__ void load(const void* base, size_t at) {
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-      v[i] = ld_stream16(static_cast<const char*>(base) + at * sizeof(T) + 16 * i);
+      v[i] = ld_dep_stream16(static_cast<const char*>(base) + at * sizeof(T) + 16 * i);
   }
   __device__ __forceinline__ float at(int i) const {
     if constexpr (sizeof(T) == 2) return bf16_at(v[0], i);
@@ -103,7 +103,7 @@ __device__ __forceinline__ void norm_row(RowGroup<kWarpRow>& g, float2 (&v)[NV][
     for (int c = 0; c < NV; ++c)
 #pragma unroll
       for (int p = 0; p < 4; p += 2) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(w + at[c] + 2 * p));
+        const float4 f = ld_dep(reinterpret_cast<const float4*>(w + at[c] + 2 * p));
         v[c][p] = __fmul2_rn(v[c][p], make_float2(f.x, f.y));
         v[c][p + 1] = __fmul2_rn(v[c][p + 1], make_float2(f.z, f.w));
       }
@@ -113,7 +113,7 @@ __device__ __forceinline__ void norm_row(RowGroup<kWarpRow>& g, float2 (&v)[NV][
     for (int c = 0; c < NV; ++c)
 #pragma unroll
       for (int p = 0; p < 4; p += 2) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(b + at[c] + 2 * p));
+        const float4 f = ld_dep(reinterpret_cast<const float4*>(b + at[c] + 2 * p));
         v[c][p] = __fadd2_rn(v[c][p], make_float2(f.x, f.y));
         v[c][p + 1] = __fadd2_rn(v[c][p + 1], make_float2(f.z, f.w));
       }
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_norm_kernel(const NormAr
   if (a.gate) {
     const uint16_t* gate = a.gate + (size_t)(a.gate_rows >= a.T ? 0 : row / a.gate_rows) * H;
 #pragma unroll
-    for (int c = 0; c < NV; ++c) gate8(__ldg(reinterpret_cast<const uint4*>(gate + at[c])), v[c]);
+    for (int c = 0; c < NV; ++c) gate8(ld_dep(reinterpret_cast<const uint4*>(gate + at[c])), v[c]);
   }
 #pragma unroll
   for (int c = 0; c < NV; ++c) residual8(a, r[c], v[c], base + at[c], (in >> c) & 1u, (in >> c) & 1u);
@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) residual_norm_rows_kernel(con
     at[c] = min(at[c], H - 8);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      pw[c][p] = a.post_w ? __ldg(reinterpret_cast<const float2*>(a.post_w + at[c]) + p) : both(1.0f);
-      qw[c][p] = a.pre_w ? __ldg(reinterpret_cast<const float2*>(a.pre_w + at[c]) + p) : both(1.0f);
+      pw[c][p] = a.post_w ? ld_dep(reinterpret_cast<const float2*>(a.post_w + at[c]) + p) : both(1.0f);
+      qw[c][p] = a.pre_w ? ld_dep(reinterpret_cast<const float2*>(a.pre_w + at[c]) + p) : both(1.0f);
     }
   }
   const float inv_n = __fdiv_rn(1.0f, (float)H);
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) residual_norm_rows_kernel(con
       if (gr != gate_row) {
         gate_row = gr;
 #pragma unroll
-        for (int c = 0; c < kRowsVec; ++c) gate[c] = __ldg(reinterpret_cast<const uint4*>(a.gate + (size_t)gr * H + at[c]));
+        for (int c = 0; c < kRowsVec; ++c) gate[c] = ld_dep(reinterpret_cast<const uint4*>(a.gate + (size_t)gr * H + at[c]));
       }
     }
     // a wait that gives up leaves the barriers of the rows to come in step: nothing more is written

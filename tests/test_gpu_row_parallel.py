@@ -556,3 +556,55 @@ def test_residual_norm_of_many_rows(T, H, kinds, gates, y_t, r_t):
     hq.hq_residual_norm(y, res2, res2, h=h, post=post, post_w=post_w, gate=gate, alpha=0.5, beta=2.0, pre=pre, pre_w=pre_w,
                         eps=1e-5)
     same(res2, out, "in place")
+
+
+# -------------------------------------------------------------------------------- one call after another
+@pytest.mark.parametrize("T,H", [(1200, 5000), (300, 2056), (40, 520)])
+def test_in_place_residuals_in_a_row(T, H):
+    """Every call reads the residual that the call ahead wrote, in lines that two rows share: the same with
+    nothing between the calls as with a wait after each."""
+    y = torch.randn(8, T, H, generator=gen(T), device=DEV).to(BF)
+    start = torch.randn(T, H, generator=gen(H), device=DEV).to(BF)
+    got = []
+    for wait in (True, False):
+        res, h = start.clone(), torch.empty(T, H, dtype=BF, device=DEV)
+        torch.cuda.synchronize()
+        for i in range(40):
+            hq.hq_residual_norm(h if i % 3 == 2 else y[i % 8], res, res, h=h if i % 3 != 2 else torch.empty_like(h),
+                                post=hq.HQ_NORM_RMS, beta=0.5)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        got.append((res, h))
+    same(got[1][0], got[0][0], "residual")
+    same(got[1][1], got[0][1], "h")
+
+
+@pytest.mark.parametrize("T", [3, 40, 200])
+def test_operands_written_just_before_the_call(T):
+    """Weights, scales and activations that the kernels just ahead in the stream are still writing."""
+    P, H, K = 2, 1032, 200
+    a, a_s, w, w_s = operands(51, P, T, H, K)
+    xs = [(torch.randn(P, T, K, generator=gen(i), device=DEV) * (i + 1)).to(BF) for i in range(12)]
+    x, q, s = torch.empty_like(xs[0]), torch.empty(P, T, 208, dtype=torch.int8, device=DEV)[..., :K], torch.empty(P, T, device=DEV)
+    ww, ws = w.clone(), w_s.clone()
+    outs = [torch.empty(P, T, H, dtype=torch.float32, device=DEV) for _ in xs]
+    ww = pitched(w, up(K, 16))[0]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        x.copy_(xs[i])
+        hq.hq_quantize_tokens(x, q, s)
+        if i % 2:
+            ww.neg_()
+        else:
+            ws.mul_(0.5)
+        hq.hq_int8_matmul(q, s, ww, ws, o)
+    torch.cuda.synchronize()
+    sign, scale = 1, w_s.clone()
+    for i, o in enumerate(outs):
+        if i % 2:
+            sign = -sign
+        else:
+            scale = scale * 0.5
+        want_q, want_s = plain_tokens(xs[i])
+        same(o, plain_product(want_q, want_s, sign * w, scale), f"call {i}")

@@ -56,7 +56,7 @@ struct DeviceInfo {
   int sms = 0;
   int qt_blocks = 0;
   bool select_smem_set = false;
-  bool pair_smem_set[3] = {};        // [output]
+  bool pair_smem_set[3][2] = {};     // [output][features 128, 256]
   bool norm_smem_set[2][2][2] = {};  // [fp32 y][fp32 residual][threads all full]
   bool few_smem_set[3][3] = {};      // [output][tokens 16, 32, 64]
   OccupancyCache dequant_tma[2][2];  // [fp32 out][bf16 shards]
@@ -593,20 +593,26 @@ hq_status raise_smem(bool& done, Kernel kern, size_t bytes) {
 constexpr size_t kSmemPerSm = 227 * 1024;
 
 template <int kOut, int kTokens>
-hq_status launch_few(const hq::MmArgs& p, const CUtensorMap& map_w, DeviceInfo& d, cudaStream_t st) {
-  CUtensorMap map_a;
-  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, kTokens, 128)) return HQ_ERR_CUDA;
+hq_status launch_few(const hq::MmArgs& p, DeviceInfo& d, cudaStream_t st) {
+  CUtensorMap map_a, map_w;
+  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, kTokens, 128) ||
+      !encode_3d(&map_w, p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.H, p.P, p.ldw, hq::kFewFeatures, 128))
+    return HQ_ERR_CUDA;
   auto kern = hq::int8_matmul_few_kernel<kOut, kTokens>;
   constexpr int kIdx = kTokens == 16 ? 0 : kTokens == 32 ? 1 : 2;
   if (raise_smem(d.few_smem_set[kOut][kIdx], kern, kSmemPerSm - 1024) != HQ_OK) return HQ_ERR_CUDA;
   // K is shared by a cluster of CTAs until they are one to an SM, or two with at least eight steps each
   // (4 ranks, 32 tokens, H = 4096, K = 1024 as a wire: 6.4 us with 128 CTAs, 7.1 with 256 of four steps;
-  // 64 tokens, 8192 x 8192: 18.2 us with 128 CTAs, 16.2 with 256).  An SM's CTAs fill its shared memory
+  // 64 tokens, 8192 x 8192: 18.2 us with 128 CTAs, 16.2 with 256), and as long as each has four steps (one
+  // token, H = 4096, K = 512: alone 3.0 us, two to a cluster 3.5, four 3.8; up to 32 tokens two steps: H = 2048,
+  // K = 1024 4.0 us, with four 4.6).  An SM's CTAs fill its shared memory
   // with their rings together (8 ranks, one token, H = 8192, K = 1024: four to an SM 12.1 us, three 15.0).
   const int kc = (int)ceil_div(p.K, hq::kMmK);
   const long long token_tiles = ceil_div(p.T, kTokens), tiles = ceil_div(p.H, hq::kFewFeatures) * token_tiles * p.P;
   int split = 1, split_log2 = 0;
-  auto fits = [&](int s) { return s <= kc && (s * tiles <= d.sms || (s * tiles <= 2 * d.sms && kc / s >= 8)); };
+  auto fits = [&](int s) {
+    return kc / s >= (kTokens == 32 ? 2 : 4) && (s * tiles <= d.sms || (s * tiles <= 2 * d.sms && kc / s >= 8));
+  };
   while (split < hq::kFewMaxSplit && fits(2 * split)) split *= 2, ++split_log2;
   const size_t red = split > 1 ? hq::few_red_bytes(kTokens) : 0;
   const int per_sm = (int)std::min<long long>(4, std::max<long long>(1, ceil_div(tiles * split, d.sms)));
@@ -617,20 +623,12 @@ hq_status launch_few(const hq::MmArgs& p, const CUtensorMap& map_w, DeviceInfo& 
   return launch_dependent(kern, grid, hq::kFewThreads, smem, st, split, map_a, map_w, p, split_log2, stages, wait_limits());
 }
 
-template <int kOut>
-hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
-  DeviceInfo* d = nullptr;
-  if (device_info(&d) != HQ_OK) return HQ_ERR_CUDA;
+template <int kOut, int kN>
+hq_status launch_pair(const hq::MmArgs& p, DeviceInfo& d, cudaStream_t st) {
   CUtensorMap map_a, map_w, map_out;
-  if (!encode_3d(&map_w, p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.H, p.P, p.ldw, hq::kMmHalf, 128)) return HQ_ERR_CUDA;
-  // Up to 64 tokens the weights are the M operand: 8 ranks, H = 8192, K = 1024 take 13.3 us at 32 tokens
-  // and 15.0 at 64 (the pair kernel: 16.7 and 17.0); 8192 x 8192 with one rank, 40 tokens 16.1 and 24.3.
-  // Beyond, the pair kernel's tiles are the faster ones: 65 tokens 17.0 us (23.2 with the weights as M
-  // and room for 128 tokens), 128 tokens 17.8 and 26.2; as a wire 21.4 and 41.1.
-  if (p.T <= 16) return launch_few<kOut, 16>(p, map_w, *d, st);
-  if (p.T <= 32) return launch_few<kOut, 32>(p, map_w, *d, st);
-  if (p.T <= 64) return launch_few<kOut, 64>(p, map_w, *d, st);
-  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, hq::kMmHalf, 128)) return HQ_ERR_CUDA;
+  if (!encode_3d(&map_a, p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.T, p.P, p.lda, hq::kMmHalf, 128) ||
+      !encode_3d(&map_w, p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.H, p.P, p.ldw, kN / 2, 128))
+    return HQ_ERR_CUDA;
   memset(&map_out, 0, sizeof map_out);
   if (kOut == hq::kMmBf16 &&
       !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.T, p.P, 2ull * p.ldo, 32, 64))
@@ -638,13 +636,31 @@ hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
   if (kOut == hq::kMmF32 &&
       !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.H, p.T, p.P, 4ull * p.ldo, 32, 64))
     return HQ_ERR_CUDA;
-  auto kern = hq::int8_matmul_pair_kernel<kOut>;
-  const size_t smem = sizeof(hq::MmSmem) + 1024;
-  if (raise_smem(d->pair_smem_set[kOut], kern, smem) != HQ_OK) return HQ_ERR_CUDA;
-  const long long tiles = (long long)p.P * ceil_div(p.T, hq::kMmTile) * ceil_div(p.H, hq::kMmTile);
-  const long long clusters = std::min<long long>(tiles, d->sms / 2);
+  auto kern = hq::int8_matmul_pair_kernel<kOut, kN>;
+  const size_t smem = sizeof(hq::MmSmem<kN>) + 1024;
+  if (raise_smem(d.pair_smem_set[kOut][kN == 256], kern, smem) != HQ_OK) return HQ_ERR_CUDA;
+  const long long tiles = (long long)p.P * ceil_div(p.T, hq::kMmTile) * ceil_div(p.H, kN);
+  const long long clusters = std::min<long long>(tiles, d.sms / 2);
   return launch_dependent(kern, dim3((unsigned)(2 * clusters)), hq::kMmThreads, smem, st, 2, map_a, map_w, map_out, p,
                           wait_limits());
+}
+
+template <int kOut>
+hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != HQ_OK) return HQ_ERR_CUDA;
+  // Up to 64 tokens the weights are the M operand: 8 ranks, H = 8192, K = 1024 take 13.3 us at 32 tokens
+  // and 15.0 at 64 (the pair kernel: 16.7 and 17.0); 8192 x 8192 with one rank, 40 tokens 16.1 and 24.3.
+  // Beyond, the pair kernel's tiles are the faster ones: 65 tokens 17.0 us (23.2 with the weights as M
+  // and room for 128 tokens), 128 tokens 17.8 and 26.2; as a wire 21.4 and 41.1.
+  if (p.T <= 16) return launch_few<kOut, 16>(p, *d, st);
+  if (p.T <= 32) return launch_few<kOut, 32>(p, *d, st);
+  if (p.T <= 64) return launch_few<kOut, 64>(p, *d, st);
+  // Tiles of 128 features as long as there is one for every pair of SMs at most (one rank, H = 4096, K = 512,
+  // 128 tokens: 4.4 us, 5.4 with 256 features; 200 tokens, 4096 x 4096: 12.2 and 14.1), else of 256 (two
+  // ranks, 700 tokens, H = 4096, K = 512: 7.5 us, 8.2 with 128; 512 tokens, H = 8192, K = 4096: 15.5 and 21.4).
+  if (p.P * ceil_div(p.T, hq::kMmTile) * ceil_div(p.H, 128) <= d->sms / 2) return launch_pair<kOut, 128>(p, *d, st);
+  return launch_pair<kOut, 256>(p, *d, st);
 }
 
 template <typename Y, typename R>

@@ -34,7 +34,7 @@ struct MmArgs {
 enum MmOut { kMmBf16 = 0, kMmF32 = 1, kMmWire = 2 };
 
 // ------------------------------------------------------------------------------------------------
-// Many tokens: a pair of CTAs to a tile of 256 tokens x 256 features.
+// Many tokens: a pair of CTAs to a tile of 256 tokens x kN features.
 //
 // tcgen05.mma with cta_group::2 takes M = 256, N = 256: each CTA of the pair loads its own 128 tokens
 // and its own 128 features (32 KB a step of K = 128 bytes) and holds the accumulators of its 128
@@ -45,17 +45,24 @@ enum MmOut { kMmBf16 = 0, kMmF32 = 1, kMmWire = 2 };
 // Warps 0-11 are the epilogue: three warps share the 32 lanes (tokens) of tensor memory that a warp can
 // read and take its chunks of 32 columns in turn, from one tile to the next.  Warp 12 loads, warp 13 of
 // the first CTA issues the products.  Every wait is bounded (hq_tma.cuh).
-constexpr int kMmTile = 256;                                   // tokens and features of a pair's tile
-constexpr int kMmHalf = 128;                                   // of one CTA
-constexpr int kMmK = 128;                                      // bytes of K a step
+//
+// kN, a tile's features, is 256 where there are tiles enough; with fewer, tiles of 128 features spread over
+// more SMs and leave half the epilogue at the end, for half as many more operand bytes a product.
+constexpr int kMmTile = 256;                              // tokens of a pair's tile
+constexpr int kMmHalf = 128;                              // of one CTA
+constexpr int kMmK = 128;                                 // bytes of K a step
 constexpr int kMmStages = 5;
 constexpr int kMmEpiWarps = 12;
-constexpr int kMmSides = kMmEpiWarps / 4;                      // epilogue warps that share 32 lanes of tensor memory
-constexpr int kMmChunks = kMmTile / 32;                        // 32 columns at a time
-constexpr int kMmWarpChunks = (kMmChunks + kMmSides - 1) / kMmSides;
+constexpr int kMmSides = kMmEpiWarps / 4;                 // epilogue warps that share 32 lanes of tensor memory
 constexpr int kMmThreads = 32 * (kMmEpiWarps + 2);
-constexpr unsigned kMmStageBytes = 2 * kMmHalf * kMmK;         // one CTA's part of a step
-constexpr int kMmGroupM = 8;                                   // token tiles that share a sweep over the features
+constexpr int kMmGroupM = 8;                              // token tiles that share a sweep over the features
+template <int kN>
+struct MmShape {
+  static_assert(kN == 128 || kN == 256, "every epilogue warp has a chunk of every tile");
+  static constexpr int kChunks = kN / 32;                 // 32 columns at a time
+  static constexpr int kWarpChunks = (kChunks + kMmSides - 1) / kMmSides;
+  static constexpr unsigned kStageBytes = (kMmHalf + kN / 2) * kMmK;  // one CTA's part of a step
+};
 
 // The parameters of 32 columns.
 struct MmCols {
@@ -64,17 +71,17 @@ struct MmCols {
   alignas(16) int zero[32];      // the wire's zero point - kMagicBits
 };
 
+template <int kN>
 struct MmSmem {
   alignas(1024) unsigned char a[kMmStages][kMmHalf * kMmK];
-  alignas(1024) unsigned char b[kMmStages][kMmHalf * kMmK];
+  alignas(1024) unsigned char b[kMmStages][kN / 2 * kMmK];
   alignas(1024) unsigned char out[kMmEpiWarps][32 * 64];       // a warp's 32 rows of 64 bytes on their way out
-  MmCols col[kMmEpiWarps][kMmWarpChunks];
+  MmCols col[kMmEpiWarps][MmShape<kN>::kWarpChunks];
   uint64_t full[kMmStages], empty[kMmStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort;
 };
-
-static_assert(sizeof(MmSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
+static_assert(sizeof(MmSmem<256>) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
 // The walk over the tiles, rank by rank.  Within a rank, groups of kMmGroupM token tiles sweep all
 // features, so that a wave of tiles shares its operands in L2.  Quotients come from fp32 reciprocals and
@@ -82,13 +89,14 @@ static_assert(sizeof(MmSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
 struct MmTileAt {
   int r, t0, n0;
 };
+template <int kN>
 struct MmWalk {
   int mt, nt, per_rank, r, j;
   float inv_group;
 
   __device__ __forceinline__ MmWalk(const MmArgs& p, int i) {
     mt = (p.T + kMmTile - 1) / kMmTile;
-    nt = (p.H + kMmTile - 1) / kMmTile;
+    nt = (p.H + kN - 1) / kN;
     per_rank = mt * nt;
     r = i / per_rank;
     j = i - r * per_rank;
@@ -104,7 +112,7 @@ struct MmWalk {
     if (rem >= kMmGroupM * nt) ++g, rem -= kMmGroupM * nt;
     const int rows = min(kMmGroupM, mt - g * kMmGroupM);
     const int n = rows == kMmGroupM ? rem / kMmGroupM : rem / rows;
-    return MmTileAt{r, (g * kMmGroupM + rem - n * rows) * kMmTile, n * kMmTile};
+    return MmTileAt{r, (g * kMmGroupM + rem - n * rows) * kMmTile, n * kN};
   }
 };
 
@@ -155,20 +163,21 @@ __device__ __forceinline__ uint32_t wire_word(const uint32_t* w, const MmCols& c
 
 // A lane's column of each of its warp's chunks, fetched a tile ahead of its use: chunk j0 + kMmSides i
 // of the 32 columns each from feature n0.
-template <int kOut>
+template <int kOut, int kN>
 struct MmFetch {
-  float scale[kMmWarpChunks], second[kMmWarpChunks];
-  int rest[kMmWarpChunks];
-  uint32_t zero[kMmWarpChunks];
+  static constexpr int kWarpChunks = MmShape<kN>::kWarpChunks, kChunks = MmShape<kN>::kChunks;
+  float scale[kWarpChunks], second[kWarpChunks];
+  int rest[kWarpChunks];
+  uint32_t zero[kWarpChunks];
 
   __device__ __forceinline__ static int column(int n0, int j0, int i, int lane) { return n0 + 32 * (j0 + kMmSides * i) + lane; }
 
   __device__ __forceinline__ void start(const MmArgs& p, int r, int n0, int j0, int lane) {
 #pragma unroll
-    for (int i = 0; i < kMmWarpChunks; ++i) {
+    for (int i = 0; i < kWarpChunks; ++i) {
       const int c = column(n0, j0, i, lane);
       const size_t g = (size_t)r * p.H + c;
-      const bool on = j0 + kMmSides * i < kMmChunks && c < p.H;
+      const bool on = j0 + kMmSides * i < kChunks && c < p.H;
       scale[i] = on ? ld_dep(p.w_scale + g) : 0.0f;
       second[i] = kOut != kMmWire && p.bias && on ? bf16_lo(ld_dep(p.bias + g)) : 0.0f;
       rest[i] = kOut == kMmWire && on && c < p.H - p.k ? ld_dep(p.rest_idx + c) : 0;
@@ -178,8 +187,8 @@ struct MmFetch {
   // The wire's grids, once the features are known.
   __device__ __forceinline__ void grids(const MmArgs& p, int r, int n0, int j0, int lane) {
 #pragma unroll
-    for (int i = 0; i < kMmWarpChunks; ++i) {
-      if (j0 + kMmSides * i >= kMmChunks || column(n0, j0, i, lane) >= p.H - p.k) continue;
+    for (int i = 0; i < kWarpChunks; ++i) {
+      if (j0 + kMmSides * i >= kChunks || column(n0, j0, i, lane) >= p.H - p.k) continue;
       const size_t g = (size_t)r * p.H + checked_index(rest[i], p.H);
       second[i] = ld_dep(p.inv_scale + g);
       zero[i] = ld_dep(p.zero + g);
@@ -187,7 +196,7 @@ struct MmFetch {
   }
   __device__ __forceinline__ void store(MmCols* s, int lane) const {
 #pragma unroll
-    for (int i = 0; i < kMmWarpChunks; ++i) {
+    for (int i = 0; i < kWarpChunks; ++i) {
       s[i].scale[lane] = scale[i];
       s[i].second[lane] = second[i];
       if (kOut == kMmWire) s[i].zero[lane] = (int)zero[i] - kMagicBits;
@@ -206,16 +215,17 @@ __device__ __forceinline__ void store_words(uint32_t* p, const uint32_t* w, int 
   }
 }
 
-template <int kOut>
+template <int kOut, int kN>
 __global__ void __launch_bounds__(kMmThreads, 1)
     int8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                             const __grid_constant__ CUtensorMap map_out, const MmArgs p, WaitLimits lim) {
   extern __shared__ unsigned char s_raw[];
-  MmSmem& sm = *reinterpret_cast<MmSmem*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kChunks = MmShape<kN>::kChunks;
+  MmSmem<kN>& sm = *reinterpret_cast<MmSmem<kN>*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cta = cluster_ctarank();
   const int step = gridDim.x / 2, first = blockIdx.x / 2;
-  MmWalk walk(p, first);
+  MmWalk<kN> walk(p, first);
   const int tiles = p.P * walk.per_rank;
   const int kc = (p.K + kMmK - 1) / kMmK;
   volatile int* abort = &sm.abort;
@@ -233,7 +243,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     sm.abort = 0;
     fence_barrier_init();
   }
-  if (warp == kMmEpiWarps + 1) tc_alloc<2>(&sm.tmem, 512);
+  if (warp == kMmEpiWarps + 1) tc_alloc<2>(&sm.tmem, 2 * kN);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -257,10 +267,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             go = false;
             break;
           }
-          if (cta == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kMmStageBytes);
+          if (cta == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * MmShape<kN>::kStageBytes);
           const uint32_t bar = cluster_addr(smem_addr(&sm.full[s]), 0);
           tma_load_3d_pair(smem_addr(sm.a[s]), &map_a, c * kMmK, at.t0 + (int)cta * kMmHalf, at.r, bar);
-          tma_load_3d_pair(smem_addr(sm.b[s]), &map_w, c * kMmK, at.n0 + (int)cta * kMmHalf, at.r, bar);
+          tma_load_3d_pair(smem_addr(sm.b[s]), &map_w, c * kMmK, at.n0 + (int)cta * (kN / 2), at.r, bar);
         }
       }
       // after an abort: the pair's loads have landed before either CTA leaves (the first CTA counts both)
@@ -272,14 +282,14 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
   } else if (warp == kMmEpiWarps + 1) {  // ---------------------------------- products
     if (cta == 0 && lane == 0) {
-      constexpr uint32_t idesc = tc_idesc(kMmTile, kMmTile);
+      constexpr uint32_t idesc = tc_idesc(kMmTile, kN);
       int i = 0, n = 0;
       bool go = true;
       for (int t = first; t < tiles && go; t += step, ++n) {
         const int b = n & 1;
         if (n >= 2 && !mbar_wait(&sm.acc_empty[b], ((n >> 1) - 1) & 1, abort, lim.producer)) break;
         tc_fence_after();
-        const uint32_t d = tmem + b * kMmTile;
+        const uint32_t d = tmem + b * kN;
         for (int c = 0; c < kc; ++c, ++i) {
           const int s = i % kMmStages;
           if (!mbar_wait(&sm.full[s], (i / kMmStages) & 1, abort, lim.consumer)) {
@@ -306,10 +316,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     MmCols* const cols_of = sm.col[warp];
     const int Hr = p.H - p.k, Wr = Hr >> 3;
     const bool wide = Hr % 32 == 0 && ((uintptr_t)p.codes & 15) == 0;  // a token's words of codes start on 16 bytes
-    MmFetch<kOut> next;
+    MmFetch<kOut, kN> next;
     float next_sa = 0.0f;
     // the warp's first chunk of its n-th tile: chunks 0, 1, .. of tile after tile go round the sides
-    auto first_chunk = [&](int n) { return (side + (kMmSides - kMmChunks % kMmSides) * n) % kMmSides; };
+    auto first_chunk = [&](int n) { return (side + (kMmSides - kChunks % kMmSides) * n) % kMmSides; };
     auto fetch = [&](const MmTileAt& at, int n) {
       const int row = at.t0 + (int)cta * kMmHalf + 32 * quad + lane;
       next_sa = row < p.T ? ld_dep(p.a_scale + (size_t)at.r * p.T + row) : 0.0f;
@@ -336,21 +346,22 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       // every lane of the warp, or none
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.acc_full[b], (n >> 1) & 1, abort, lim.consumer))) break;
       tc_fence_after();
-      const uint32_t acc = tmem + b * kMmTile + ((uint32_t)(32 * quad) << 16);
+      const uint32_t acc = tmem + b * kN + ((uint32_t)(32 * quad) << 16);
       const bool live = row + lane < p.T;
       uint32_t* const words =
           kOut == kMmWire ? p.codes + ((size_t)cur.r * p.T + row + lane) * Wr + (cur.n0 >> 3) : nullptr;
+      int i = 0;
 #pragma unroll 1
-      for (int chunk = first_chunk(n), i = 0; chunk < kMmChunks; chunk += kMmSides, ++i) {
+      for (int chunk = first_chunk(n); chunk < kChunks; chunk += kMmSides, ++i) {
         const MmCols& cols = cols_of[i];
         uint32_t v[32];
         tc_load(acc + 32 * chunk, v);
-        if (chunk + kMmSides >= kMmChunks) {  // the warp's last read of the tile: its columns may be written again
+        if (chunk + kMmSides >= kChunks) {  // the warp's last read of the tile: its columns may be written again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&sm.acc_empty[b]), 0));
         }
-        if (kOut == kMmWire && i == 1 && more) next.grids(p, at.r, at.n0, first_chunk(n + 1), lane);
+        if (kOut == kMmWire && kChunks > 4 && i == 1 && more) next.grids(p, at.r, at.n0, first_chunk(n + 1), lane);
         const int n0 = cur.n0 + 32 * chunk;
         if (n0 >= p.H || row >= p.T) continue;
         float f[32];
@@ -410,6 +421,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           }
         }
       }
+      if (kOut == kMmWire && kChunks <= 4 && more) next.grids(p, at.r, at.n0, first_chunk(n + 1), lane);
     }
     if (kOut != kMmWire && lane == 0) tma_store_wait();
   }
@@ -418,7 +430,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   __syncthreads();
   cluster_sync();  // neither CTA's memory goes while the other still counts on it
   tc_fence_after();
-  if (warp == kMmEpiWarps + 1) tc_dealloc<2>(tmem, 512);
+  if (warp == kMmEpiWarps + 1) tc_dealloc<2>(tmem, 2 * kN);
 }
 
 // ------------------------------------------------------------------------------------------------

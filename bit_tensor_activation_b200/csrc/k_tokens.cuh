@@ -1,8 +1,10 @@
 // k_tokens.cuh -- a bf16 row to int8 with one scale a token: the activations of a row-parallel
 // product in 8-bit integers.
 //
-// A row is read once and stays in registers between its maximum and its codes.  HBM-bound: 2 bytes
-// read and 1 written an element, 4 bytes written a row.
+// A row is read once and stays in registers between its maximum and its codes: up to 1024 elements in one
+// warp (no barrier), longer ones in a CTA.  HBM-bound: 2 bytes read and 1 written an element, 4 bytes
+// written a row; 65536 rows of 1024 take 31.6 us, 6.4 TB/s (a copy: 6.55).  A few rows take 1.4 to 2.0 us,
+// which is a launch and two round trips to memory.
 #pragma once
 
 #include "hq_rows.cuh"

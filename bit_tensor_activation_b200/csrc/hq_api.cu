@@ -56,7 +56,7 @@ struct DeviceInfo {
   int sms = 0;
   int qt_blocks = 0;
   bool select_smem_set = false;
-  bool pair_smem_set[3][2] = {};     // [output][features 128, 256]
+  bool pair_smem_set[3][2][2] = {};  // [output][features 128, 256][wide codes]
   bool norm_smem_set[2][2][2] = {};  // [fp32 y][fp32 residual][threads all full]
   bool few_smem_set[3][3] = {};      // [output][tokens 16, 32, 64]
   OccupancyCache dequant_tma[2][2];  // [fp32 out][bf16 shards]
@@ -636,9 +636,11 @@ hq_status launch_pair(const hq::MmArgs& p, DeviceInfo& d, cudaStream_t st) {
   if (kOut == hq::kMmF32 &&
       !encode_3d(&map_out, p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.H, p.T, p.P, 4ull * p.ldo, 32, 64))
     return HQ_ERR_CUDA;
-  auto kern = hq::int8_matmul_pair_kernel<kOut, kN>;
+  // a token's words of codes start on 16 bytes (no other output has them)
+  const bool wide = kOut != hq::kMmWire || ((p.H - p.k) % 32 == 0 && aligned(p.codes, 16));
+  auto kern = wide ? hq::int8_matmul_pair_kernel<kOut, kN, true> : hq::int8_matmul_pair_kernel<kOut, kN, kOut != hq::kMmWire>;
   const size_t smem = sizeof(hq::MmSmem<kN>) + 1024;
-  if (raise_smem(d.pair_smem_set[kOut][kN == 256], kern, smem) != HQ_OK) return HQ_ERR_CUDA;
+  if (raise_smem(d.pair_smem_set[kOut][kN == 256][wide], kern, smem) != HQ_OK) return HQ_ERR_CUDA;
   const long long tiles = (long long)p.P * ceil_div(p.T, hq::kMmTile) * ceil_div(p.H, kN);
   const long long clusters = std::min<long long>(tiles, d.sms / 2);
   return launch_dependent(kern, dim3((unsigned)(2 * clusters)), hq::kMmThreads, smem, st, 2, map_a, map_w, map_out, p,

@@ -212,18 +212,37 @@ struct MmFetch {
   }
 };
 
-// `n` words of one token's codes.
-__device__ __forceinline__ void store_words(uint32_t* p, const uint32_t* w, int n, bool wide) {
-  if (n == 4 && wide) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
+// A warp's 32 tokens' four words of codes each (x: the lane's token's, at words): `n` words of `rows` tokens,
+// `pitch` words apart.  kWide (a token's words start on 16 bytes): one store a token.  Else through 512 bytes
+// at `stage`, four lanes to a token, since single words straight from the lanes that hold them touch 32 lines
+// with every store (8 ranks, 4096 tokens, H = 4104, K = 512: 121 us, 147 so; kWide, H = 4096: 105).
+template <bool kWide>
+__device__ __forceinline__ void store_words(uint32_t* words, int pitch, const uint32_t (&x)[4], int n, int rows,
+                                            uint32_t stage, int lane) {
+  if constexpr (kWide) {
+    if (lane >= rows) return;
+    if (n == 4) {
+      *reinterpret_cast<uint4*>(words) = make_uint4(x[0], x[1], x[2], x[3]);
+      return;
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = w[i];
+    for (int i = 0; i < 3; ++i)
+      if (i < n) words[i] = x[i];
+  } else {
+    __syncwarp();
+    st_shared16(stage + 16 * lane, x[0], x[1], x[2], x[3]);
+    __syncwarp();
+    const int w = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      const uint32_t v = ld_shared(stage + 16 * r + 4 * w);
+      if (r < rows && w < n) words[(long long)(r - lane) * pitch + w] = v;
+    }
   }
 }
 
-template <int kOut, int kN>
+template <int kOut, int kN, bool kWide>
 __global__ void __launch_bounds__(kMmThreads, 1)
     int8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                             const __grid_constant__ CUtensorMap map_out, const MmArgs p, WaitLimits lim) {
@@ -323,7 +342,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const uint32_t stage = smem_addr(sm.out[warp]);
     MmCols* const cols_of = sm.col[warp];
     const int Hr = p.H - p.k, Wr = Hr >> 3;
-    const bool wide = Hr % 32 == 0 && ((uintptr_t)p.codes & 15) == 0;  // a token's words of codes start on 16 bytes
     MmFetch<kOut, kN> next;
     float next_sa = 0.0f;
     // the warp's first chunk of its n-th tile: chunks 0, 1, .. of tile after tile go round the sides
@@ -416,7 +434,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             uint32_t x[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) x[q] = wire_word(w + 4 * q, cols, 8 * q);
-            if (live) store_words(words + 4 * chunk, x, min(4, (Hr - n0) >> 3), wide);
+            store_words<kWide>(words + 4 * chunk, Wr, x, min(4, (Hr - n0) >> 3), p.T - row, stage, lane);
           }
           if (kOut == kMmWire && live && n0 + 32 > Hr) {  // kept features: 32 tokens of one lie beside one another
             uint16_t* s = p.side + (size_t)cur.r * p.k * p.T + row + lane;

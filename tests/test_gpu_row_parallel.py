@@ -608,3 +608,24 @@ def test_operands_written_just_before_the_call(T):
             scale = scale * 0.5
         want_q, want_s = plain_tokens(xs[i])
         same(o, plain_product(want_q, want_s, sign * w, scale), f"call {i}")
+
+
+@pytest.mark.parametrize("T", [20, 300])
+@pytest.mark.parametrize("shift", [1, 2, 4, 8])
+def test_codes_that_start_anywhere(T, shift):
+    """The codes need no more than 4-byte alignment, whatever their rows' length allows."""
+    P, H, K, k = 2, 544, 96, 32
+    a, a_s, w, w_s = operands(61, P, T, H, K)
+    keep, rest, zero = selection(62, P, H, k)
+    inv = torch.full((P, H), 1e-2, device=DEV)
+    order = torch.cat([rest, keep]).long()
+    wo, so = w[:, order].contiguous(), w_s[:, order].contiguous()
+    n = P * T * (H - k) // 8
+    want = torch.empty(P, T, (H - k) // 8, dtype=torch.int32, device=DEV), torch.empty(P, k, T, dtype=BF, device=DEV)
+    hq.hq_quantize_pack(plain_product(a, a_s, w, w_s).to(BF), keep, rest, inv, zero, *want)
+    buf = torch.full((n + 16,), 0x77, dtype=torch.int32, device=DEV)
+    codes, side = buf[shift:shift + n].view_as(want[0]), torch.empty_like(want[1])
+    hq.hq_int8_matmul_pack(a, a_s, wo, so, keep, rest, inv, zero, codes, side)
+    same(codes, want[0], "codes")
+    same(side, want[1], "side")
+    assert (buf[:shift] == 0x77).all() and (buf[shift + n:] == 0x77).all()

@@ -542,18 +542,27 @@ hq_status quantize_tokens_entry(const uint16_t* x, int ldx, int64_t rows, int K,
   if (rows > 0 && (!x || !q || !scale)) return HQ_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return HQ_ERR_MISALIGNED;
   if (rows == 0) return HQ_OK;
-  const RowShape s = row_shape(K);
-  const dim3 grid((unsigned)(s.warp ? ceil_div(rows, 4) : rows));
   const long long n = rows;
+  const int nvec = (int)ceil_div(K, 8);
   cudaStream_t st = (cudaStream_t)stream;
-  auto go = [&](auto kern) { return launch_dependent(kern, grid, s.threads, 0, st, 1, x, ldx, n, K, q, ldq, scale); };
-  if (s.warp) return s.nv == 1 ? go(hq::quantize_tokens_kernel<1, true>)
-                  : s.nv == 2  ? go(hq::quantize_tokens_kernel<2, true>)
-                               : go(hq::quantize_tokens_kernel<4, true>);
-  return s.nv == 1   ? go(hq::quantize_tokens_kernel<1, false>)
-         : s.nv == 2 ? go(hq::quantize_tokens_kernel<2, false>)
-         : s.nv == 4 ? go(hq::quantize_tokens_kernel<4, false>)
-                     : go(hq::quantize_tokens_kernel<8, false>);
+  auto go = [&](auto kern, long long ctas, int threads) {
+    return launch_dependent(kern, dim3((unsigned)ctas), threads, 0, st, 1, x, ldx, n, K, q, ldq, scale);
+  };
+  auto cta = [&](int nv) { return (int)(32 * ceil_div(ceil_div(nvec, nv), 32)); };
+  if (nvec <= 8) return go(hq::quantize_tokens_kernel<1, 8>, ceil_div(n, 16), 128);
+  if (nvec <= 16) return go(hq::quantize_tokens_kernel<2, 8>, ceil_div(n, 16), 128);
+  if (nvec <= 32) return go(hq::quantize_tokens_kernel<4, 8>, ceil_div(n, 16), 128);
+  if (nvec <= 64) return go(hq::quantize_tokens_kernel<2, 32>, ceil_div(n, 4), 128);
+  if (nvec <= 128) return go(hq::quantize_tokens_kernel<4, 32>, ceil_div(n, 4), 128);
+  DeviceInfo* d = nullptr;
+  if (device_info(&d) != HQ_OK) return HQ_ERR_CUDA;
+  // Longer rows: one load a thread where rows are few, for the shortest chain; with more rows a warp holds up
+  // to 2048 elements (32768 rows: 31.5 us, a CTA with one load a thread 49), and a CTA has four loads a thread
+  // (8192 rows of 8192: 36 us, 59 with one) and above 8192 elements eight (8192 rows of 14336: 61 us, 75 with four).
+  if (n < 4LL * d->sms && nvec <= hq::kRowMaxThreads) return go(hq::quantize_tokens_kernel<1, 0>, n, cta(1));
+  if (nvec <= 256) return go(hq::quantize_tokens_kernel<8, 32>, ceil_div(n, 4), 128);
+  if (nvec <= 1024) return go(hq::quantize_tokens_kernel<4, 0>, n, cta(4));
+  return go(hq::quantize_tokens_kernel<8, 0>, n, cta(8));
 }
 
 // The checks that the two products share.

@@ -629,3 +629,21 @@ def test_codes_that_start_anywhere(T, shift):
     same(codes, want[0], "codes")
     same(side, want[1], "side")
     assert (buf[:shift] == 0x77).all() and (buf[shift + n:] == 0x77).all()
+
+
+@pytest.mark.parametrize("rows,K", [(1000, 9), (1001, 64), (999, 100), (1003, 128), (777, 250), (700, 256), (1201, 1500),
+                                    (1200, 2048), (700, 2049), (640, 4097), (601, 8192), (600, 8193), (600, 20000)])
+def test_token_codes_of_many_rows(rows, K):
+    """Rows enough for every way in which a row's elements are shared, with rows over at the end."""
+    g = gen(rows + K)
+    x = (torch.randn(rows, K, generator=g, device=DEV) * torch.exp(2 * torch.randn(rows, 1, generator=g, device=DEV))).to(BF)
+    x[rows // 2] = 0
+    x[rows - 1, K - 1] = float("nan")
+    xv, _ = pitched(x, up(K, 8) + 8, 7.0)
+    q, buf = pitched(torch.full((rows + 1, K), 99, dtype=torch.int8, device=DEV), up(K, 16) + 16, 99)
+    s = torch.full((rows + 1,), -1.0, device=DEV)
+    hq.hq_quantize_tokens(xv, q[:rows], s[:rows])
+    want_q, want_s = plain_tokens(x)
+    same(q[:rows], want_q, "codes")
+    same(s[:rows], want_s, "scales")
+    assert s[rows] == -1 and (buf[:, K:] == 99).all() and (buf[rows] == 99).all(), "written outside"

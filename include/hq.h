@@ -265,7 +265,9 @@ hq_status hq_two_step_reduce_noalloc(const uint16_t* x, int P, int T, int H, int
  * A row-parallel layer in 8-bit integers around the path above: what makes the partial sums, and
  * what follows their sum.  The pages give no arithmetic for either (sections "The Challenge of
  * Quantization" and "Combating Quantization Errors with Tensor Parallelism" place the compressed
- * sum behind a row-parallel product); the readings R23..R25 are stated here.
+ * sum behind a row-parallel product); the readings R23..R25 are stated here.  The four calls may
+ * begin their set-up under the kernel ahead of them in the stream; they read and write memory only
+ * once that kernel is complete.
  *
  * hq_quantize_tokens (R23): rows of bf16 to int8 with one scale a row.  For row t with
  * amax = max_k |x[t][k]|:

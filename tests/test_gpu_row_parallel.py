@@ -647,3 +647,67 @@ def test_token_codes_of_many_rows(rows, K):
     same(q[:rows], want_q, "codes")
     same(s[:rows], want_s, "scales")
     assert s[rows] == -1 and (buf[:, K:] == 99).all() and (buf[rows] == 99).all(), "written outside"
+
+
+# -------------------------------------------------------------------------------- what the documentation allows besides
+def test_tokens_of_any_rank():
+    """[..., K]: a single row without a leading dimension, and rows in three of them."""
+    x = torch.randn(40, generator=gen(1), device=DEV).to(BF)
+    q, s = torch.empty(48, dtype=torch.int8, device=DEV)[:40], torch.empty((), device=DEV)
+    hq.hq_quantize_tokens(x, q, s)
+    want_q, want_s = plain_tokens(x[None])
+    same(q, want_q[0], "codes")
+    same(s[None], want_s, "scale")
+    x = torch.randn(2, 3, 5, 64, generator=gen(2), device=DEV).to(BF)
+    q, s = torch.empty(2, 3, 5, 64, dtype=torch.int8, device=DEV), torch.empty(2, 3, 5, device=DEV)
+    hq.hq_quantize_tokens(x, q, s)
+    want_q, want_s = plain_tokens(x)
+    same(q, want_q, "codes")
+    same(s, want_s, "scales")
+    with pytest.raises(ValueError):  # rows that are not one pitch apart
+        hq.hq_quantize_tokens(x.transpose(0, 1), q.transpose(0, 1), torch.empty(3, 2, 5, device=DEV))
+
+
+def test_no_rows_of_a_wire():
+    a, a_s, w, w_s = operands(71, 2, 0, 64, 32)
+    keep, rest, zero = selection(72, 2, 64, 8)
+    hq.hq_int8_matmul_pack(a, a_s, w, w_s, keep, rest, torch.ones(2, 64, device=DEV), zero,
+                           torch.empty(2, 0, 7, dtype=torch.int32, device=DEV), torch.empty(2, 8, 0, dtype=BF, device=DEV))
+
+
+@pytest.mark.parametrize("T,H,rows", [(10, 64, 4), (1301, 8192, 100), (500, 4096, 499)])
+def test_gate_rows_that_do_not_divide_the_tokens(T, H, rows):
+    """The C call's gate has ceil(T / gate_rows) rows, the last of them for what is left."""
+    G = -(-T // rows)
+    y, res, gate = (torch.randn(n, H, generator=gen(n + H), device=DEV).to(BF) for n in (T, T + 1, G))
+    res = res[:T]
+    out, h = torch.empty(T, H, dtype=BF, device=DEV), torch.empty(T, H, dtype=BF, device=DEV)
+    torch.cuda.synchronize()
+    st = hq.lib().hq_residual_norm(y.data_ptr(), 0, res.data_ptr(), out.data_ptr(), 0, T, H, 0, None, None, gate.data_ptr(),
+                                   rows, 1.0, 1.0, 1, None, None, 1e-6, h.data_ptr(), None, 0, None, None)
+    assert st == hq.HQ_OK
+    torch.cuda.synchronize()
+    u = gate.to(D)[torch.arange(T, device=DEV) // rows] * y.to(D)
+    close(out, res.to(D) + u, res.to(D).abs() + u.abs(), "residual")
+
+
+def test_bits_and_parameters_as_tensors():
+    """bf16 tensors may be passed as their bits, and weights as parameters that ask for gradients."""
+    a, a_s, w, w_s = operands(81, 1, 5, 64, 48)
+    out = torch.empty(1, 5, 64, dtype=torch.int16, device=DEV)
+    hq.hq_int8_matmul(a, a_s, w, torch.nn.Parameter(w_s), out)
+    same(out.view(BF), plain_product(a, a_s, w, w_s).to(BF), "out")
+
+
+def test_many_features():
+    """The largest number of features of a product."""
+    P, T, H, K = 1, 3, hq.HQ_INT8_MAX_H, 32
+    a, a_s, w, w_s = operands(91, P, T, H, K)
+    out = torch.empty(P, T, H, dtype=BF, device=DEV)
+    hq.hq_int8_matmul(a, a_s, w, w_s, out)
+    same(out, plain_product(a, a_s, w, w_s).to(BF), "few tokens")
+    T = 70
+    a, a_s, w, w_s = operands(92, P, T, H, K)
+    out = torch.empty(P, T, H, dtype=BF, device=DEV)
+    hq.hq_int8_matmul(a, a_s, w, w_s, out)
+    same(out, plain_product(a, a_s, w, w_s).to(BF), "more tokens")

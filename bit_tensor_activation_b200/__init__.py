@@ -170,13 +170,11 @@ def _check(status, where):
         raise HQError(status, where)
 
 
-def _done(status, where):
-    """Whether _hqargs made the call (whose error is raised here)."""
-    if status is None:
-        return False
-    if status != HQ_OK:
+def _failed(status, where):
+    """After a call through _hqargs that did not return HQ_OK: raises the library's error; None (an argument
+    does not fit) goes on to the checks in Python."""
+    if status is not None:
         raise HQError(status, where)
-    return True
 
 
 def _handle(stream):
@@ -226,9 +224,10 @@ def _dequant_args(codes, side, keep_idx, rest_idx, scale, zero, out, stream):
 
 
 def hq_dequant_reduce(codes, side, keep_idx, rest_idx, scale, zero, out, stream=None) -> None:
-    if _done(_hqargs.dequant_reduce(codes, side, keep_idx, rest_idx, scale, zero, out, _handle(stream)),
-             "hq_dequant_reduce"):
+    st = _hqargs.dequant_reduce(codes, side, keep_idx, rest_idx, scale, zero, out, stream and _handle(stream))
+    if st == HQ_OK:
         return
+    _failed(st, "hq_dequant_reduce")
     _check(_lib.hq_dequant_reduce(*_dequant_args(codes, side, keep_idx, rest_idx, scale, zero, out, stream)),
            "hq_dequant_reduce")
 
@@ -431,8 +430,10 @@ def _call(fn, where, dev, stream, *args):
 def hq_quantize_tokens(x, q, scale, stream=None) -> None:
     """x [..., K] bf16 to int8 q [..., K] with one scale a row, scale [...] f32; the rows of x and q
     may be further apart than K (multiples of 8 and 16 elements)."""
-    if _done(_hqargs.quantize_tokens(x, q, scale, _handle(stream)), "hq_quantize_tokens"):
+    st = _hqargs.quantize_tokens(x, q, scale, stream and _handle(stream))
+    if st == HQ_OK:
         return
+    _failed(st, "hq_quantize_tokens")
     dev = _device_of(x, "x")
     shape = x.shape
     lead, rows = shape[:-1], 1
@@ -448,8 +449,10 @@ def hq_int8_matmul(a, a_scale, w, w_scale, out, bias=None, stream=None) -> None:
     """Every rank's partial sum out [P, T, H] (bf16 or f32) of int8 activations a [P, T, K] with a
     scale a token (a_scale [P, T]) and int8 weights w [P, H, K] with a scale a channel (w_scale
     [P, H]); bias [P, H] bf16.  The rows of a, w and out may be further apart than K and H."""
-    if _done(_hqargs.int8_matmul(a, a_scale, w, w_scale, out, bias, _handle(stream)), "hq_int8_matmul"):
+    st = _hqargs.int8_matmul(a, a_scale, w, w_scale, out, bias, stream and _handle(stream))
+    if st == HQ_OK:
         return
+    _failed(st, "hq_int8_matmul")
     dev = _device_of(a, "a")
     P, T, K = a.shape
     H = w.shape[1]
@@ -466,9 +469,11 @@ def hq_int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, z
     """The wire (codes, side) of the partial sums that hq_int8_matmul would write, bit for bit as
     hq_quantize_pack makes it.  w and w_scale have their rows in the wire's order:
     torch.cat([rest_idx, keep_idx]) of the features' own."""
-    if _done(_hqargs.int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, zero, codes, side,
-                                      _handle(stream)), "hq_int8_matmul_pack"):
+    st = _hqargs.int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, zero, codes, side,
+                                  stream and _handle(stream))
+    if st == HQ_OK:
         return
+    _failed(st, "hq_int8_matmul_pack")
     dev = _device_of(a, "a")
     P, T, K = a.shape
     H = w.shape[1]
@@ -489,9 +494,11 @@ def hq_residual_norm(y, res, res_out, h=None, q=None, q_scale=None, post=HQ_NORM
     int8 with one scale a row (q, q_scale).  y, res, res_out, h [T, H] (y and res bf16 or f32; res_out
     of res's type, res itself allowed); q [T, H] int8, rows may be further apart; weights and biases
     [H] f32; gate [G, H] bf16 with G a divisor of T: row t uses gate row t // (T // G)."""
-    if _done(_hqargs.residual_norm(y, res, res_out, h, q, q_scale, post, post_w, post_b, gate, alpha, beta, pre, pre_w,
-                                   pre_b, eps, _handle(stream)), "hq_residual_norm"):
+    st = _hqargs.residual_norm(y, res, res_out, h, q, q_scale, post, post_w, post_b, gate, alpha, beta, pre, pre_w, pre_b,
+                               eps, stream and _handle(stream))
+    if st == HQ_OK:
         return
+    _failed(st, "hq_residual_norm")
     dev = _device_of(y, "y")
     T, H = shape = y.shape
     vector = (H,)

@@ -522,19 +522,6 @@ hq_status two_step_entry(const uint16_t* x, int P, int T, int H, int k, const in
   return launch_dequant<float, false>(src, 1, Tb, H, k2, keep2, scale2, zero2, out, H, (cudaStream_t)stream, *d, P);
 }
 
-// A row of n elements over threads: vectors of 8 a thread (NV) and threads a row; 32 threads: a warp
-// to a row, four rows to a CTA.
-struct RowShape {
-  int nv, threads;
-  bool warp;
-};
-RowShape row_shape(int n) {
-  const int nvec = (int)ceil_div(n, 8);
-  if (nvec <= 4 * 32) return RowShape{nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, 128, true};
-  const int nv = nvec <= hq::kRowMaxThreads ? 1 : nvec <= 2 * hq::kRowMaxThreads ? 2 : nvec <= 4 * hq::kRowMaxThreads ? 4 : 8;
-  return RowShape{nv, (int)(32 * ceil_div(ceil_div(nvec, nv), 32)), false};
-}
-
 hq_status quantize_tokens_entry(const uint16_t* x, int ldx, int64_t rows, int K, int8_t* q, int ldq, float* scale,
                                 void* stream) {
   if (rows < 0 || K < 1 || K > HQ_INT8_MAX_K || !ld_ok(ldx, K) || ldq < K || ldq % 16 != 0) return HQ_ERR_INVALID_ARG;
@@ -676,12 +663,11 @@ hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
 
 template <typename Y, typename R>
 hq_status launch_norm(const hq::NormArgs& a, DeviceInfo& d, cudaStream_t st) {
-  const RowShape s = row_shape(a.H);
-  const dim3 rows((unsigned)a.T), fours((unsigned)ceil_div(a.T, 4));
-  if (s.warp && s.nv == 1) return launch_dependent(hq::residual_norm_kernel<Y, R, 1, 128, true>, fours, 128, 0, st, 1, a);
-  if (s.warp && s.nv == 2) return launch_dependent(hq::residual_norm_kernel<Y, R, 2, 128, true>, fours, 128, 0, st, 1, a);
-  if (s.warp) return launch_dependent(hq::residual_norm_kernel<Y, R, 4, 128, true>, fours, 128, 0, st, 1, a);
   const int nvec = a.H / 8;
+  const dim3 rows((unsigned)a.T), fours((unsigned)ceil_div(a.T, 4));
+  if (nvec <= 32) return launch_dependent(hq::residual_norm_kernel<Y, R, 1, 128, true>, fours, 128, 0, st, 1, a);
+  if (nvec <= 64) return launch_dependent(hq::residual_norm_kernel<Y, R, 2, 128, true>, fours, 128, 0, st, 1, a);
+  if (nvec <= 128) return launch_dependent(hq::residual_norm_kernel<Y, R, 4, 128, true>, fours, 128, 0, st, 1, a);
   auto threads = [&](int nv) { return (int)(32 * ceil_div(ceil_div(nvec, nv), 32)); };
   // Which kernel, by what was measured (bf16, gate, both weights): the row ring from 4096 < H <= 8192 and
   // eight rows an SM on (8192 x 8192: 99 us, a CTA a row 120; 1500 x 8192: 25.6 and 26.1; 777 x 8192: 16.9

@@ -665,8 +665,11 @@ template <typename Y, typename R>
 hq_status launch_norm(const hq::NormArgs& a, DeviceInfo& d, cudaStream_t st) {
   const int nvec = a.H / 8;
   const dim3 rows((unsigned)a.T), fours((unsigned)ceil_div(a.T, 4));
+  // Up to 1024 elements a row to a warp, with no more vectors a lane than it takes (65536 x 656 bf16: 62 us with
+  // three, 82 with room for four); beyond, a CTA a row (32768 x 2048: 97 us, a warp with eight 121).
   if (nvec <= 32) return launch_dependent(hq::residual_norm_kernel<Y, R, 1, 128, true>, fours, 128, 0, st, 1, a);
   if (nvec <= 64) return launch_dependent(hq::residual_norm_kernel<Y, R, 2, 128, true>, fours, 128, 0, st, 1, a);
+  if (nvec <= 96) return launch_dependent(hq::residual_norm_kernel<Y, R, 3, 128, true>, fours, 128, 0, st, 1, a);
   if (nvec <= 128) return launch_dependent(hq::residual_norm_kernel<Y, R, 4, 128, true>, fours, 128, 0, st, 1, a);
   auto threads = [&](int nv) { return (int)(32 * ceil_div(ceil_div(nvec, nv), 32)); };
   // Which kernel, by what was measured (bf16, gate, both weights): the row ring from 4096 < H <= 8192 and

@@ -313,7 +313,7 @@ def close(got, want, mag, what):
 
 
 NORM_SHAPES = [(1, 8), (3, 16), (5, 256), (2, 264), (9, 520), (4, 1024), (7, 1032), (1, 4096), (32, 8192), (3, 5000),
-               (2, 8200), (5, 16384), (2, 32768), (300, 2048)]
+               (2, 8200), (5, 16384), (2, 32768), (300, 2048), (6, 656), (5, 768), (4, 776)]
 
 
 @pytest.mark.parametrize("kinds", [("none", "rms"), ("rms", "rms"), ("layer", "layer"), ("rms", "none"), ("layer", "rms")],

@@ -604,19 +604,16 @@ __global__ void __launch_bounds__(kFewThreads)
     fence_barrier_init();
   }
   if (warp == 5) tc_alloc<1>(&s_tmem, kColumns);
-  if (warp == 4 && lane == 0) {
-    prefetch_tensor_map(&map_a);
-    prefetch_tensor_map(&map_w);
-  }
+  // the weights start on their way into L2 under the kernel that makes the activations (whatever it writes
+  // goes through L2 as well, so this brings nothing stale)
+  if (warp == 4 && lane < c1 - c0) tma_prefetch_3d(&map_w, (c0 + lane) * kMmK, n0, r);
+  if (warp == 4 && lane == 0) prefetch_tensor_map(&map_a);
   tc_fence_before();
   __syncthreads();
   if (split > 1) cluster_arrive();  // here: this CTA's memory may be written
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   grid_trigger();
-  // the weights start on their way into L2 under the kernel that makes the activations (whatever it writes
-  // goes through L2 as well, so this brings nothing stale)
-  if (warp == 4 && lane < c1 - c0) tma_prefetch_3d(&map_w, (c0 + lane) * kMmK, n0, r);
   grid_wait();
 
   if (warp == 4) {  // ---------------------------------------------------------- loads

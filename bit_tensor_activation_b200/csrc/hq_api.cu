@@ -597,12 +597,12 @@ hq_status launch_few(const hq::MmArgs& p, DeviceInfo& d, cudaStream_t st) {
   auto kern = hq::int8_matmul_few_kernel<kOut, kTokens>;
   constexpr int kIdx = kTokens == 16 ? 0 : kTokens == 32 ? 1 : 2;
   if (raise_smem(d.few_smem_set[kOut][kIdx], kern, kSmemPerSm - 1024) != HQ_OK) return HQ_ERR_CUDA;
-  // K is shared by a cluster of CTAs until they are one to an SM, or two with at least eight steps each
-  // (4 ranks, 32 tokens, H = 4096, K = 1024 as a wire: 6.4 us with 128 CTAs, 7.1 with 256 of four steps;
-  // 64 tokens, 8192 x 8192: 18.2 us with 128 CTAs, 16.2 with 256), and as long as each has four steps (one
-  // token, H = 4096, K = 512: alone 3.0 us, two to a cluster 3.5, four 3.8; up to 32 tokens two steps: H = 2048,
-  // K = 1024 4.0 us, with four 4.6).  An SM's CTAs fill its shared memory
-  // with their rings together (8 ranks, one token, H = 8192, K = 1024: four to an SM 12.1 us, three 15.0).
+  // K is shared by a cluster of CTAs until they are one to an SM (4 ranks, 32 tokens, H = 4096, K = 1024 as a
+  // wire: 7.3 us with 128 CTAs, 7.7 with 256), or two with at least eight steps each (64 tokens, 8192 x 8192:
+  // 15.7 us with 256 CTAs, 15.8 with 128), and as long as each has four steps (one token, H = 4096, K = 512:
+  // alone 3.0 us, two to a cluster 3.4, four 3.7; up to 32 tokens two steps: H = 2048, K = 1024 4.1 us, with
+  // four 4.6).  An SM's CTAs fill its shared memory with their rings together (8 ranks, one token, H = 8192,
+  // K = 1024: four to an SM 12.7 us, three 14.7).
   const int kc = (int)ceil_div(p.K, hq::kMmK);
   const long long token_tiles = ceil_div(p.T, kTokens), tiles = ceil_div(p.H, hq::kFewFeatures) * token_tiles * p.P;
   int split = 1, split_log2 = 0;
@@ -647,10 +647,10 @@ template <int kOut>
 hq_status launch_matmul(const hq::MmArgs& p, cudaStream_t st) {
   DeviceInfo* d = nullptr;
   if (device_info(&d) != HQ_OK) return HQ_ERR_CUDA;
-  // Up to 64 tokens the weights are the M operand: 8 ranks, H = 8192, K = 1024 take 13.3 us at 32 tokens
-  // and 15.0 at 64 (the pair kernel: 16.7 and 17.0); 8192 x 8192 with one rank, 40 tokens 16.1 and 24.3.
+  // Up to 64 tokens the weights are the M operand: 8 ranks, H = 8192, K = 1024 take 13.7 us at 32 tokens
+  // and 15.6 at 64 (the pair kernel: 16.4 and 16.9); 8192 x 8192 with one rank, 40 tokens 15.6 and 21.6.
   // Beyond, the pair kernel's tiles are the faster ones: 65 tokens 17.0 us (23.2 with the weights as M
-  // and room for 128 tokens), 128 tokens 17.8 and 26.2; as a wire 21.4 and 41.1.
+  // and room for 128 tokens), 128 tokens 17.7 and 26.2; as a wire 21.4 and 41.1.
   if (p.T <= 16) return launch_few<kOut, 16>(p, *d, st);
   if (p.T <= 32) return launch_few<kOut, 32>(p, *d, st);
   if (p.T <= 64) return launch_few<kOut, 64>(p, *d, st);

@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 // each and their int32 sums meet in distributed shared memory: CTA q adds up the columns q kTokens / S ..
 // of all S of them.  Sums of integers do not depend on the order.
 //
-// Weights from memory, 8 ranks, H = 8192, K = 1024: 12.1 us with one token and 13.3 with 32, 5.5 and 5.0 TB/s
+// Weights from memory, 8 ranks, H = 8192, K = 1024: 12.7 us with one token and 13.7 with 32, 5.3 and 4.9 TB/s
 // of weights; one rank, H = 4096, K = 512, one token: 3.0 us, of which the weights' bytes are 0.3.
 //
 // Warps 0-3 are the epilogue, warp 4 loads, warp 5 issues the products.
@@ -604,10 +604,10 @@ __global__ void __launch_bounds__(kFewThreads)
     fence_barrier_init();
   }
   if (warp == 5) tc_alloc<1>(&s_tmem, kColumns);
-  // the weights start on their way into L2 under the kernel that makes the activations (whatever it writes
-  // goes through L2 as well, so this brings nothing stale)
-  if (warp == 4 && lane < c1 - c0) tma_prefetch_3d(&map_w, (c0 + lane) * kMmK, n0, r);
-  if (warp == 4 && lane == 0) prefetch_tensor_map(&map_a);
+  if (warp == 4 && lane == 0) {
+    prefetch_tensor_map(&map_a);
+    prefetch_tensor_map(&map_w);
+  }
   tc_fence_before();
   __syncthreads();
   if (split > 1) cluster_arrive();  // here: this CTA's memory may be written

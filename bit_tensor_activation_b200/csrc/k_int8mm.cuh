@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       for (int chunk = first_chunk(n); chunk < kChunks; chunk += kMmSides, ++i) {
         const MmCols& cols = cols_of[i];
         uint32_t v[32];
+        __syncwarp();  // a chunk ends in work of single lanes, tc_load takes the whole warp
         tc_load(acc + 32 * chunk, v);
         if (chunk + kMmSides >= kChunks) {  // the warp's last read of the tile: its columns may be written again
           tc_fence_before();
@@ -659,6 +660,7 @@ __global__ void __launch_bounds__(kFewThreads)
   if (warp < 4) {  // ------------------------------------------------------------ epilogue
     for (int j = threadIdx.x; j < kTokens; j += 128)
       s_scale[j] = t0 + j < p.T ? ld_dep(p.a_scale + (size_t)r * p.T + t0 + j) : 0.0f;
+    __syncwarp();
     named_barrier_sync(128);
     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_acc, 0, abort, lim.consumer)) && !*abort;
     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -668,6 +670,7 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll 1
       for (int j = 0; j < kTokens && t0 + j < p.T; j += kGroup) {
         uint32_t v[kGroup];
+        __syncwarp();  // emit's stores are those of single lanes, tc_load takes the whole warp
         tc_load(acc + j, v);
         feature.emit(v, t0 + j, kGroup, smem_addr(s_scale + j));
       }
@@ -689,8 +692,8 @@ __global__ void __launch_bounds__(kFewThreads)
       }
     }
   }
+  __syncwarp();  // the roles of warps 4 and 5 are one lane's, the barrier is the whole warp's
   if (split > 1 && (warp >= 4 || !ok)) cluster_wait();
-  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (split > 1) {

@@ -1,0 +1,73 @@
+"""Where the row-parallel layer's kernels and calls can go wrong besides their sizes: lanes of a warp that
+part ways, waits that run out at any moment, sizes past 32 bits, arguments of every kind.
+
+Plain forms and tolerances are those of test_gpu_row_parallel.py: codes, products and wires are compared
+for equality.
+"""
+import pytest
+import torch
+
+import bit_tensor_activation_b200 as hq
+from gpu_helpers import DEV, assert_no_device_error
+from test_gpu_row_parallel import BF, operands, plain_product, same, selection
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _errors_are_clear():
+    hq.hq_read_device_error()
+    yield
+    assert_no_device_error()
+
+
+def wire_problem(seed, P, T, H, K, k, inv=1e-2):
+    """A product's operands, the wire's parameters and the weights in the wire's order."""
+    a, a_s, w, w_s = operands(seed, P, T, H, K)
+    keep, rest, zero = selection(seed, P, H, k)
+    order = torch.cat([rest, keep]).long()
+    wo = torch.zeros(P, H, -(-K // 16) * 16, dtype=torch.int8, device=DEV)
+    wo[..., :K] = w[:, order]
+    return a, a_s, w, w_s, wo[..., :K], w_s[:, order].contiguous(), keep, rest, torch.full((P, H), inv, device=DEV), zero
+
+
+def empty_wire(P, T, H, k):
+    return (torch.empty(P, T, (H - k) // 8, dtype=torch.int32, device=DEV), torch.empty(P, k, T, dtype=BF, device=DEV))
+
+
+def check_wire(problem, k):
+    a, a_s, w, w_s, wo, so, keep, rest, inv, zero = problem
+    P, T, H = a.shape[0], a.shape[1], w.shape[1]
+    want, got = empty_wire(P, T, H, k), empty_wire(P, T, H, k)
+    hq.hq_quantize_pack(plain_product(a, a_s, w, w_s).to(BF), keep, rest, inv, zero, *want)
+    hq.hq_int8_matmul_pack(a, a_s, wo, so, keep, rest, inv, zero, *got)
+    same(got[0], want[0], "codes")
+    same(got[1], want[1], "side")
+
+
+# -------------------------------------------------------------------------------- lanes that part ways
+@pytest.mark.parametrize("P,T,H,K,k", [(2, 300, 1056, 200, 40), (3, 70, 528, 96, 16), (1, 1001, 4096, 256, 64),
+                                       (2, 33, 1032, 300, 264), (1, 64, 256, 1100, 8), (1, 5, 512, 4100, 16)])
+def test_single_lanes_take_the_rare_path(P, T, H, K, k):
+    """Every third token has a huge scale, every seventh is not a number, and kept features and the last
+    tokens end within a warp: neighbouring lanes take different paths through one chunk after another."""
+    problem = wire_problem(T + H, P, T, H, K, k)
+    problem[1][:, ::3] *= 1e6
+    problem[1][:, ::7] = float("nan")
+    for _ in range(20):
+        check_wire(problem, k)
+
+
+@pytest.mark.parametrize("P,T,H,K", [(1, 1, 128, 4096), (1, 3, 264, 2048), (2, 16, 1000, 1024), (1, 20, 520, 1500),
+                                     (1, 33, 4096, 8192), (1, 64, 1032, 4096), (1, 9, 512, 65536)])
+def test_clusters_of_every_size(P, T, H, K):
+    """K over two, four and eight CTAs, whose load and product warps come to the cluster's barrier from one
+    lane's loop; the last features and tokens end within a warp."""
+    a, a_s, w, w_s = operands(T + K, P, T, H, K)
+    bias = torch.randn(P, H, device=DEV).to(BF)
+    for t in (BF, torch.float32):
+        want = plain_product(a, a_s, w, w_s, bias).to(t)
+        for _ in range(20):
+            out = torch.full((P, T, H), 9.0, dtype=t, device=DEV)
+            hq.hq_int8_matmul(a, a_s, w, w_s, out, bias=bias)
+            same(out, want, "out")

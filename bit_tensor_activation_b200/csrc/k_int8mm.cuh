@@ -88,6 +88,8 @@ struct MmSmem {
   uint64_t full[kMmStages], empty[kMmStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int abort;
+  uint32_t gave_up[2];                                         // of both CTAs, once their roles are done
+  uint32_t issued[2];                                          // and the steps each of them has loaded
 };
 static_assert(sizeof(MmSmem<256>) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
@@ -242,6 +244,30 @@ __device__ __forceinline__ void store_words(uint32_t* words, int pitch, const ui
   }
 }
 
+// After a wait that gave up, in either CTA: what is in flight is done before either of them leaves.  Loads are
+// counted on the first CTA's barriers, both CTAs' parts of a step together.  A step that only one CTA has loaded
+// (they give up apart by a few steps, never by more than the ring) is made up to its whole count here: the
+// first CTA has announced both parts, the second none.  Only the last step of each stage can be under way, since a
+// stage is loaded anew once its products are done.
+template <int kN>
+__device__ __noinline__ void mm_pair_drain(MmSmem<kN>& sm, int warp, int lane, uint32_t cta, WaitLimits lim) {
+  if (cta != 0 || lane != 0) return;
+  int ignore = 0;
+  if (warp == kMmEpiWarps) {
+    const int mine = (int)sm.issued[0], other = (int)sm.issued[1], most = max(mine, other);
+    for (int j = max(0, most - kMmStages); j < most; ++j) {
+      uint64_t* const full = &sm.full[j % kMmStages];
+      if (j >= mine) mbar_arrive_expect_tx(full, MmShape<kN>::kStageBytes);
+      if (j >= other) mbar_complete_tx(full, MmShape<kN>::kStageBytes);
+      mbar_wait(full, (j / kMmStages) & 1, &ignore, lim.producer);
+    }
+  }
+  if (warp == kMmEpiWarps + 1) {  // the lane that issued the products
+    tc_commit<2>(&sm.drain);
+    mbar_wait(&sm.drain, 0, &ignore, lim.producer);
+  }
+}
+
 template <int kOut, int kN, bool kWide>
 __global__ void __launch_bounds__(kMmThreads, 1)
     int8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
@@ -256,6 +282,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   const int tiles = p.P * walk.per_rank;
   const int kc = (p.K + kMmK - 1) / kMmK;
   volatile int* abort = &sm.abort;
+  int issued = 0;  // the load lane's steps
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMmStages; ++s) {
@@ -284,13 +311,12 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       prefetch_tensor_map(&map_a);
       prefetch_tensor_map(&map_w);
       producer_start_delay(lim.start_delay);
-      int i = 0;
       bool go = true;
       for (int t = first; t < tiles && go; t += step, walk.advance(step)) {
         const MmTileAt at = walk.at();
-        for (int c = 0; c < kc; ++c, ++i) {
-          const int s = i % kMmStages;
-          if (i >= kMmStages && !mbar_wait(&sm.empty[s], ((i / kMmStages) - 1) & 1, abort, lim.producer)) {
+        for (int c = 0; c < kc; ++c, ++issued) {
+          const int s = issued % kMmStages;
+          if (issued >= kMmStages && !mbar_wait(&sm.empty[s], ((issued / kMmStages) - 1) & 1, abort, lim.producer)) {
             go = false;
             break;
           }
@@ -299,12 +325,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           tma_load_3d_pair(smem_addr(sm.a[s]), &map_a, c * kMmK, at.t0 + (int)cta * kMmHalf, at.r, bar);
           tma_load_3d_pair(smem_addr(sm.b[s]), &map_w, c * kMmK, at.n0 + (int)cta * (kN / 2), at.r, bar);
         }
-      }
-      // after an abort: the pair's loads have landed before either CTA leaves (the first CTA counts both)
-      if (*abort && cta == 0) {
-        int ignore = 0;
-        for (int j = max(0, i - kMmStages); j < i; ++j)
-          mbar_wait(&sm.full[j % kMmStages], (j / kMmStages) & 1, &ignore, lim.producer);
       }
     }
   } else if (warp == kMmEpiWarps + 1) {  // ---------------------------------- products
@@ -330,11 +350,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           tc_commit<2>(&sm.empty[s]);
         }
         if (go) tc_commit<2>(&sm.acc_full[b]);
-      }
-      if (*abort) {  // the products in flight are done before tensor memory is freed
-        int ignore = 0;
-        tc_commit<2>(&sm.drain);
-        mbar_wait(&sm.drain, 0, &ignore, lim.producer);
       }
     }
   } else {  // ------------------------------------------------------------------ epilogue
@@ -455,7 +470,22 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  // All roles are done and the CTA's own abort flag is final; both CTAs learn both flags and counts.
+  if (warp == kMmEpiWarps && lane == 0) {
+    const uint32_t gave_up = *abort != 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      st_cluster(cluster_addr(smem_addr(&sm.gave_up[cta]), q), gave_up);
+      st_cluster(cluster_addr(smem_addr(&sm.issued[cta]), q), (uint32_t)issued);
+    }
+  }
+  __syncwarp();
   cluster_sync();  // neither CTA's memory goes while the other still counts on it
+  if (sm.gave_up[0] | sm.gave_up[1]) {  // in both CTAs or in none
+    mm_pair_drain(sm, warp, lane, cta, lim);
+    __syncwarp();
+    cluster_sync();
+  }
   tc_fence_after();
   if (warp == kMmEpiWarps + 1) tc_dealloc<2>(tmem, 2 * kN);
 }
@@ -594,6 +624,7 @@ __global__ void __launch_bounds__(kFewThreads)
   const int kc = (p.K + kMmK - 1) / kMmK;
   const int c0 = (kc * rank) >> split_log2, c1 = (kc * (rank + 1)) >> split_log2;
   volatile int* abort = &s_abort;
+  int issued = 0;  // the load lane's steps
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -620,7 +651,7 @@ __global__ void __launch_bounds__(kFewThreads)
   if (warp == 4) {  // ---------------------------------------------------------- loads
     if (lane == 0) {
       producer_start_delay(lim.start_delay);
-      int s = 0, phase = 1, issued = 0;
+      int s = 0, phase = 1;
       for (int c = c0; c < c1; ++c, ++issued) {
         if (issued >= stages && !mbar_wait(&s_empty[s], phase, abort, lim.producer)) break;
         unsigned char* at = base + s * few_stage_bytes(kTokens);
@@ -628,11 +659,6 @@ __global__ void __launch_bounds__(kFewThreads)
         tma_load_3d(smem_addr(at), &map_w, c * kMmK, n0, r, smem_addr(&s_full[s]));
         tma_load_3d(smem_addr(at + kFewFeatures * kMmK), &map_a, c * kMmK, t0, r, smem_addr(&s_full[s]));
         if (++s == stages) s = 0, phase ^= 1;
-      }
-      if (*abort) {  // the loads in flight have landed before the CTA leaves
-        int ignore = 0;
-        for (int j = max(0, issued - stages); j < issued; ++j)
-          mbar_wait(&s_full[j % stages], (j / stages) & 1, &ignore, lim.producer);
       }
     }
   } else if (warp == 5) {  // ---------------------------------------------------- products
@@ -649,9 +675,7 @@ __global__ void __launch_bounds__(kFewThreads)
         tc_commit<1>(&s_empty[s]);
         if (++s == stages) s = 0, phase ^= 1;
       }
-      tc_commit<1>(&s_acc);  // also after an abort: the products in flight are done before tensor memory is freed
-      int ignore = 0;
-      if (*abort) mbar_wait(&s_acc, 0, &ignore, lim.producer);
+      tc_commit<1>(&s_acc);  // also after an abort
     }
   }
   FewFeature<kOut> feature(p, r, warp < 4 ? n0 + 32 * warp + lane : p.H);
@@ -696,6 +720,16 @@ __global__ void __launch_bounds__(kFewThreads)
   if (split > 1 && (warp >= 4 || !ok)) cluster_wait();
   tc_fence_before();
   __syncthreads();
+  // All roles are done and the abort flag is final.  After a wait that gave up: the loads in flight have landed
+  // before the CTA leaves, and the products are done before tensor memory is freed.
+  if (*abort && lane == 0) {
+    int ignore = 0;
+    if (warp == 4)
+      for (int j = max(0, issued - stages); j < issued; ++j)
+        mbar_wait(&s_full[j % stages], (j / stages) & 1, &ignore, lim.producer);
+    if (warp == 5) mbar_wait(&s_acc, 0, &ignore, lim.producer);
+  }
+  __syncwarp();
   if (split > 1) {
     cluster_sync();  // all parts of this CTA's columns are here
     if (warp < 4 && ok) {

@@ -71,3 +71,56 @@ def test_clusters_of_every_size(P, T, H, K):
             out = torch.full((P, T, H), 9.0, dtype=t, device=DEV)
             hq.hq_int8_matmul(a, a_s, w, w_s, out, bias=bias)
             same(out, want, "out")
+
+
+# -------------------------------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("what", ["few, its steps within the ring", "few", "few of a cluster", "pair, one tile", "pair",
+                                  "pair, a tile's steps within the ring", "pair wire"])
+def test_waits_that_run_out_at_any_moment(what):
+    """Producers held back by 1 us to 0.5 ms, consumers that give up after about 0.2 ms: in some launches the
+    wait runs out ahead of the loads, in some beside them, in some after the last of them was issued or in one
+    CTA of several alone.  A launch either gives the result or reports HQ_ERR_TIMEOUT, with nothing of it under
+    way when its CTAs leave, and the next one is right."""
+    P, T, H, K = {"few, its steps within the ring": (2, 5, 8192, 300), "few": (8, 20, 8192, 3000),
+                  "few of a cluster": (1, 9, 512, 4096), "pair, one tile": (1, 256, 256, 5000), "pair": (2, 600, 4096, 1500),
+                  "pair, a tile's steps within the ring": (1, 100, 512, 600), "pair wire": (1, 700, 2048, 256)}[what]
+    wire, k = what.endswith("wire"), 8
+    problem = wire_problem(3, P, T, H, K, k)
+    a, a_s, w, w_s, wo, so, keep, rest, inv, zero = problem
+    want = plain_product(a, a_s, w, w_s).to(BF)
+    if wire:
+        codes, side = empty_wire(P, T, H, k)
+        hq.hq_quantize_pack(want, keep, rest, inv, zero, codes, side)
+        got = empty_wire(P, T, H, k)
+    else:
+        out = torch.empty(P, T, H, dtype=BF, device=DEV)
+
+    def call():
+        if wire:
+            hq.hq_int8_matmul_pack(a, a_s, wo, so, keep, rest, inv, zero, *got)
+        else:
+            hq.hq_int8_matmul(a, a_s, w, w_s, out)
+
+    def check():
+        if wire:
+            same(got[0], codes, "codes")
+            same(got[1], side, "side")
+        else:
+            same(out, want, "out")
+
+    assert_no_device_error()
+    seen = []
+    for delay in [2_000] + list(range(100_000, 500_000, 10_000)) + [1_000_000]:
+        hq.hq_selftest_set_pipeline_stall(20_000, delay)
+        try:
+            call()
+            seen.append(hq.hq_read_device_error())
+        finally:
+            hq.hq_selftest_set_pipeline_stall(0, 0)
+        assert seen[-1] in (hq.HQ_OK, hq.HQ_ERR_TIMEOUT), hq.hq_status_string(seen[-1])
+        if seen[-1] == hq.HQ_OK:
+            check()
+        call()
+        assert_no_device_error()
+        check()
+    assert seen[-1] == hq.HQ_ERR_TIMEOUT

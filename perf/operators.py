@@ -142,7 +142,7 @@ def _buffers(c):
     if c["op"] == "norm":
         b["h"] = new(T, H)
     if c["op"] == "layer":
-        b["hq"], b["hs"] = new(1, T, H, dtype=torch.int8), new(1, T, dtype=torch.float32)
+        b["hq"], b["hs"] = new(1, T, -(-H // 16) * 16, dtype=torch.int8)[..., :H], new(1, T, dtype=torch.float32)
         b["up"] = new(1, T, c["F"])
     return b
 

@@ -105,7 +105,7 @@ struct MmWalk {
   float inv_group;
 
   __device__ __forceinline__ MmWalk(const MmArgs& p, int i) {
-    mt = (p.T + kMmTile - 1) / kMmTile;
+    mt = (p.T - 1) / kMmTile + 1;  // T >= 1; T + 255 may pass 2^31
     nt = (p.H + kN - 1) / kN;
     per_rank = mt * nt;
     r = i / per_rank;

@@ -124,3 +124,34 @@ def test_waits_that_run_out_at_any_moment(what):
         assert_no_device_error()
         check()
     assert seen[-1] == hq.HQ_ERR_TIMEOUT
+
+
+# -------------------------------------------------------------------------------- sizes at the limits of an int
+def test_the_most_tokens():
+    """T = 2^31 - 1, the largest that the call takes, as the narrowest wire (52 GB in all)."""
+    P, T, H, K = 1, 2 ** 31 - 1, 8, 16
+    if torch.cuda.mem_get_info()[0] < 60e9:
+        pytest.skip("needs 60 GB of free memory")
+    a = torch.zeros(P, T, K, dtype=torch.int8, device=DEV)
+    a_s = torch.ones(P, T, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    w = torch.randint(-127, 128, (P, H, K), generator=g, device=DEV, dtype=torch.int8)
+    w_s = torch.ones(P, H, device=DEV)
+    ends = (slice(0, 300), slice(2 ** 30 - 150, 2 ** 30 + 150), slice(T - 300, T))
+    for e in ends:
+        a[:, e] = torch.randint(-127, 128, (P, 300, K), generator=g, device=DEV, dtype=torch.int8)
+    keep, rest = torch.empty(0, dtype=torch.int32, device=DEV), torch.arange(H, dtype=torch.int32, device=DEV)
+    inv = torch.full((P, H), 1e-4, device=DEV)
+    zero = torch.arange(1, 9, dtype=torch.uint8, device=DEV).repeat(P, 2)[:, :H].contiguous()
+    codes, side = torch.full((P, T, 1), 0x5A5A5A5A, dtype=torch.int32, device=DEV), torch.empty(P, 0, T, dtype=BF, device=DEV)
+    hq.hq_int8_matmul_pack(a, a_s, w, w_s, keep, rest, inv, zero, codes, side)
+    for e in ends:
+        want = empty_wire(P, 300, H, 0)
+        hq.hq_quantize_pack(plain_product(a[:, e], a_s[:, e], w, w_s).to(BF), keep, rest, inv, zero, *want)
+        same(codes[:, e], want[0], "codes")
+        assert len(want[0].unique()) > 100
+        codes[:, e] = 0x87654321 - (1 << 32)  # the code of a row of zeros: the zero points
+    for at in range(0, T, 1 << 28):
+        assert (codes[:, at:at + (1 << 28)] == 0x87654321 - (1 << 32)).all()
+    del a, a_s, codes
+    torch.cuda.empty_cache()

@@ -9,7 +9,7 @@ import torch
 
 import bit_tensor_activation_b200 as hq
 from gpu_helpers import DEV, assert_no_device_error
-from test_gpu_row_parallel import BF, operands, plain_product, same, selection
+from test_gpu_row_parallel import BF, layer, layer_problem, operands, plain_product, same, selection
 
 pytestmark = pytest.mark.gpu
 
@@ -155,3 +155,27 @@ def test_the_most_tokens():
         assert (codes[:, at:at + (1 << 28)] == 0x87654321 - (1 << 32)).all()
     del a, a_s, codes
     torch.cuda.empty_cache()
+
+# -------------------------------------------------------------------------------- again and again
+@pytest.mark.parametrize("P,T,H,K,k,F", [(7, 1200, 280, 208, 0, 64), (3, 20, 1112, 272, 56, 616), (2, 700, 4104, 128, 40, 128)])
+def test_a_layer_repeats_itself_bit_for_bit(P, T, H, K, k, F):
+    """The same inputs give the same bits in every pass, alone and between passes on other inputs."""
+    pairs = [list(layer_problem(seed, P, T, H, K, k, F)[0]) for seed in (31, 32)]
+    for args in pairs:  # the product after the norm takes rows a multiple of 16 bytes apart
+        args[-1]["q"] = torch.empty(T, -(-H // 16) * 16, dtype=torch.int8, device=DEV)[:, :H]
+        rows = torch.zeros(*args[5].shape[:2], -(-H // 16) * 16, dtype=torch.int8, device=DEV)
+        rows[..., :H] = args[5]
+        args[5] = rows[..., :H]
+    results = ("sum", "res", "q_s", "up", "codes")
+    first = []
+    for args in pairs:
+        layer(*args)
+        torch.cuda.synchronize()
+        first.append({n: args[-1][n].clone() for n in results})
+    for i in range(30):
+        for args, want in zip(pairs, first):
+            layer(*args)
+            if i % 3 == 0:
+                layer(*args)
+            for n in results:
+                same(args[-1][n], want[n], n)

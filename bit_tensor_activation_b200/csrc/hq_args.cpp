@@ -125,12 +125,18 @@ struct Args {
   }
 };
 
-// The library's call on the arguments' device.
+// The library's call on the arguments' device.  Python's lock is not held meanwhile (a tenth of a microsecond):
+// a launch waits where the stream's queue is full, and what it waits for may be a thread that needs the lock.
+// `call` touches no Python object.
 template <typename Call>
 PyObject* run(Args& a, Call call) {
   if (!a.ok) Py_RETURN_NONE;
   const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(a.dev)));
-  return PyLong_FromLong(call());
+  hq_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = call();
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
 }
 
 // A method as Python calls it.  A tensor without storage or with symbolic sizes throws when it is asked for
@@ -261,8 +267,9 @@ PyObject* residual_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const auto* pre_b = static_cast<const float*>(a.dense(14, kF32, {H}, true));
   void* st = a.stream(16);
   const int iT = a.size(T), iH = a.size(H), ig = a.size(gate_rows);
+  const hq_out_dtype ydt = a.f32(0) ? HQ_OUT_F32 : HQ_OUT_BF16;
   return run(a, [&] {
-    return hq_residual_norm(py, a.f32(0) ? HQ_OUT_F32 : HQ_OUT_BF16, pr, po, f32 ? HQ_OUT_F32 : HQ_OUT_BF16, iT, iH,
+    return hq_residual_norm(py, ydt, pr, po, f32 ? HQ_OUT_F32 : HQ_OUT_BF16, iT, iH,
                             static_cast<hq_norm_kind>(post), post_w, post_b, gate, ig, alpha, beta,
                             static_cast<hq_norm_kind>(pre), pre_w, pre_b, eps, ph, pq, ldq, pqs, st);
   });

@@ -179,3 +179,59 @@ def test_a_layer_repeats_itself_bit_for_bit(P, T, H, K, k, F):
                 layer(*args)
             for n in results:
                 same(args[-1][n], want[n], n)
+
+
+# -------------------------------------------------------------------------------- other threads of the program
+LOCK_SHIM = r"""
+#define _GNU_SOURCE
+#include <dlfcn.h>
+#include <stdio.h>
+static int note(const char* name) {
+  int (*held)(void) = (int (*)(void))dlsym(RTLD_DEFAULT, "PyGILState_Check");
+  printf("%s %s\n", name, held && held() ? "held" : "free");
+  fflush(stdout);
+  return 0;
+}
+#define CALL(name) int name(void) { return note(#name); }
+CALL(hq_quantize_tokens)
+CALL(hq_int8_matmul)
+CALL(hq_int8_matmul_pack)
+CALL(hq_dequant_reduce)
+CALL(hq_residual_norm)
+"""
+LOCK_PROGRAM = r"""
+import torch
+import bit_tensor_activation_b200 as hq
+new = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")
+P, T, H, K, k = 2, 4, 64, 32, 8
+i8, i32, u8, f32 = torch.int8, torch.int32, torch.uint8, torch.float32
+a, a_s, w, w_s = new(P, T, K, dtype=i8), new(P, T, dtype=f32), new(P, H, K, dtype=i8), new(P, H, dtype=f32)
+keep, rest, grid, zero = new(k, dtype=i32), new(H - k, dtype=i32), new(P, H, dtype=f32), new(P, H, dtype=u8)
+codes, side, out = new(P, T, (H - k) // 8, dtype=i32), new(P, k, T), new(T, H)
+hq.hq_quantize_tokens(new(P, T, K), a, a_s)
+hq.hq_int8_matmul(a, a_s, w, w_s, new(P, T, H))
+hq.hq_int8_matmul_pack(a, a_s, w, w_s, keep, rest, grid, zero, codes, side)
+hq.hq_dequant_reduce(codes, side, keep, rest, grid, zero, out)
+hq.hq_residual_norm(out, out, out, h=new(T, H))
+"""
+
+
+def test_launches_leave_pythons_lock_to_other_threads(tmp_path):
+    """The library's calls are replaced by ones that launch nothing and say whether Python's lock is held."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+
+    if not shutil.which("gcc"):
+        pytest.skip("needs a C compiler")
+    (tmp_path / "shim.c").write_text(LOCK_SHIM)
+    shim = str(tmp_path / "shim.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", str(tmp_path / "shim.c"), "-o", shim, "-ldl"], check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(hq.__file__)))
+    r = subprocess.run([sys.executable, "-c", LOCK_PROGRAM], cwd=root, env=dict(os.environ, LD_PRELOAD=shim), text=True,
+                       capture_output=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+    said = dict(line.split() for line in r.stdout.splitlines() if line.startswith("hq_"))
+    assert said == {n: "free" for n in ("hq_quantize_tokens", "hq_int8_matmul", "hq_int8_matmul_pack", "hq_dequant_reduce",
+                                        "hq_residual_norm")}, said

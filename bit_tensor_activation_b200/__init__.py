@@ -5,7 +5,8 @@ library's CUDA kernels.  The functions carry the C names and take torch tensors 
 used for device memory and streams): each tensor is checked for device, dtype, shape and
 contiguity, and its data pointer is passed with the current CUDA stream.  A nonzero status
 raises ``HQError``.  There is no CPU fallback: importing this package on a machine without the
-built ``libhq.so`` raises.
+built ``libhq.so`` raises.  The checks of the calls that matter for few tokens are also there in C++
+(``_hqargs.so``); without that, the same checks run in Python.
 
 Shapes (P ranks, T rows, H features, k kept features, H' = H - k):
   x [P, T, H] bf16; ema_min/ema_max [P, H] f32; keep_idx [k] i32; rest_idx [H'] i32;
@@ -20,18 +21,35 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libhq.so")
 
-for _so in (LIB_PATH, os.path.join(_PKG, "_hqargs.so")):
-    if not os.path.exists(_so):
-        raise ImportError(f"{_so} is not built: run `python bit_tensor_activation_b200/build.py` "
-                          "(there is no CPU fallback)")
+if not os.path.exists(LIB_PATH):
+    raise ImportError(f"{LIB_PATH} is not built: run `python bit_tensor_activation_b200/build.py` "
+                      "(there is no CPU fallback)")
 
-from . import _hqargs  # noqa: E402
+
+class _NoArgs:
+    """In the place of _hqargs where it does not load: no argument fits, so that every call goes on to the
+    checks in Python and from there to libhq.so."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    quantize_tokens = int8_matmul = int8_matmul_pack = dequant_reduce = residual_norm = _none
+
+
+try:
+    from . import _hqargs
+except ImportError as _e:  # not built, or built for another Python or torch
+    _hqargs = _NoArgs
+    warnings.warn(f"the argument checks in C++ do not load ({_e}): calls check in Python, which takes 4 to 7 us more "
+                  "each (run `python bit_tensor_activation_b200/build.py`)", RuntimeWarning, stacklevel=2)
 
 _lib = ctypes.CDLL(LIB_PATH)
 _vp, _i32, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float

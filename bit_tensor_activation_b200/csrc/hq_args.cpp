@@ -9,6 +9,9 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
+
+#include <cstring>
 
 #include "hq.h"
 
@@ -281,6 +284,23 @@ PyMethodDef methods[] = {HQ_METHOD(quantize_tokens), HQ_METHOD(int8_matmul),   H
                          HQ_METHOD(dequant_reduce),  HQ_METHOD(residual_norm), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hqargs", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
+// The module reads tensors by torch's C++ layout: it is for the Python and torch that it was built with.
+bool built_for_this() {
+  if ((Py_Version >> 16) != (PY_VERSION_HEX >> 16)) {
+    PyErr_SetString(PyExc_ImportError, "_hqargs.so was built for Python " PY_VERSION);
+    return false;
+  }
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  const char* v = version && PyUnicode_Check(version) ? PyUnicode_AsUTF8(version) : nullptr;
+  const size_t n = sizeof(TORCH_VERSION) - 1;
+  const bool same = v && strncmp(v, TORCH_VERSION, n) == 0 && (v[n] == 0 || v[n] == '+');
+  Py_XDECREF(version);
+  Py_XDECREF(torch);
+  if (!same && !PyErr_Occurred()) PyErr_SetString(PyExc_ImportError, "_hqargs.so was built for torch " TORCH_VERSION);
+  return same;
+}
+
 }  // namespace
 
-PyMODINIT_FUNC PyInit__hqargs() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__hqargs() { return built_for_this() ? PyModule_Create(&module) : nullptr; }

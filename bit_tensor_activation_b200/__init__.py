@@ -395,6 +395,13 @@ def _dense(t, dev, dtypes, shape, name):
     return p
 
 
+def _int(n, name):
+    """A number that the C ABI takes as an int: ctypes would cut a larger one to its low 32 bits."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} is {n}: more than an int holds")
+    return n
+
+
 def _pitched(t, dev, dtypes, shape, multiple, name):
     """(pointer, row pitch in elements) of a tensor [..., n] on device `dev` whose rows are dense and one
     pitch apart.  The strides of dimensions of one element do not count; a tensor of at most one row
@@ -409,7 +416,7 @@ def _pitched(t, dev, dtypes, shape, multiple, name):
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.numel():
-        return None, -(-n // multiple) * multiple
+        return None, _int(-(-n // multiple) * multiple, f"{name}'s row pitch")
     st = t.stride()
     if st[-1] != 1 and n > 1:
         raise ValueError(f"{name}: rows must be dense")
@@ -421,7 +428,7 @@ def _pitched(t, dev, dtypes, shape, multiple, name):
             elif s != rows * ld:
                 raise ValueError(f"{name}: rows must be one pitch apart")
             rows *= n_
-    return t.data_ptr(), -(-n // multiple) * multiple if ld is None else ld
+    return t.data_ptr(), _int(-(-n // multiple) * multiple if ld is None else ld, f"{name}'s row pitch")
 
 
 def _device_of(t, name):
@@ -459,7 +466,7 @@ def hq_quantize_tokens(x, q, scale, stream=None) -> None:
         rows *= n
     px, ldx = _pitched(x, dev, _BF16, shape, 8, "x")
     pq, ldq = _pitched(q, dev, _I8, shape, 16, "q")
-    _call(_lib.hq_quantize_tokens, "hq_quantize_tokens", dev, stream, px, ldx, rows, shape[-1], pq, ldq,
+    _call(_lib.hq_quantize_tokens, "hq_quantize_tokens", dev, stream, px, ldx, rows, _int(shape[-1], "K"), pq, ldq,
           _dense(scale, dev, _F32, lead, "scale"))
 
 
@@ -478,8 +485,8 @@ def hq_int8_matmul(a, a_scale, w, w_scale, out, bias=None, stream=None) -> None:
     pw, ldw = _pitched(w, dev, _I8, (P, H, K), 16, "w")
     po, ldo = _pitched(out, dev, _BF16_F32, (P, T, H), 8, "out")
     _call(_lib.hq_int8_matmul, "hq_int8_matmul", dev, stream, pa, lda, _dense(a_scale, dev, _F32, (P, T), "a_scale"), pw,
-          ldw, _dense(w_scale, dev, _F32, (P, H), "w_scale"), _dense(bias, dev, _BF16, (P, H), "bias"), P, T, H, K, po,
-          ldo, HQ_OUT_F32 if out.dtype == torch.float32 else HQ_OUT_BF16)
+          ldw, _dense(w_scale, dev, _F32, (P, H), "w_scale"), _dense(bias, dev, _BF16, (P, H), "bias"), _int(P, "P"),
+          _int(T, "T"), _int(H, "H"), _int(K, "K"), po, ldo, HQ_OUT_F32 if out.dtype == torch.float32 else HQ_OUT_BF16)
 
 
 def hq_int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, zero, codes, side,
@@ -499,9 +506,10 @@ def hq_int8_matmul_pack(a, a_scale, w, w_scale, keep_idx, rest_idx, inv_scale, z
     pa, lda = _pitched(a, dev, _I8, (P, T, K), 16, "a")
     pw, ldw = _pitched(w, dev, _I8, (P, H, K), 16, "w")
     _call(_lib.hq_int8_matmul_pack, "hq_int8_matmul_pack", dev, stream, pa, lda,
-          _dense(a_scale, dev, _F32, (P, T), "a_scale"), pw, ldw, _dense(w_scale, dev, _F32, (P, H), "w_scale"), P, T, H,
-          K, k, _dense(keep_idx, dev, _I32, (k,), "keep_idx"), _dense(rest_idx, dev, _I32, (H - k,), "rest_idx"),
-          _dense(inv_scale, dev, _F32, (P, H), "inv_scale"), _dense(zero, dev, _U8, (P, H), "zero"),
+          _dense(a_scale, dev, _F32, (P, T), "a_scale"), pw, ldw, _dense(w_scale, dev, _F32, (P, H), "w_scale"),
+          _int(P, "P"), _int(T, "T"), _int(H, "H"), _int(K, "K"), _int(k, "k"), _dense(keep_idx, dev, _I32, (k,), "keep_idx"),
+          _dense(rest_idx, dev, _I32, (H - k,), "rest_idx"), _dense(inv_scale, dev, _F32, (P, H), "inv_scale"),
+          _dense(zero, dev, _U8, (P, H), "zero"),
           _dense(codes, dev, _CODES, (P, T, (H - k) // 8), "codes"), _dense(side, dev, _BF16, (P, k, T), "side"))
 
 
@@ -532,10 +540,11 @@ def hq_residual_norm(y, res, res_out, h=None, q=None, q_scale=None, post=HQ_NORM
     pq, ldq = (None, 0) if q is None else _pitched(q, dev, _I8, shape, 16, "q")
     _call(_lib.hq_residual_norm, "hq_residual_norm", dev, stream, _dense(y, dev, _BF16_F32, shape, "y"),
           HQ_OUT_F32 if y.dtype == torch.float32 else HQ_OUT_BF16, _dense(res, dev, _BF16_F32, shape, "res"),
-          _dense(res_out, dev, _BF16_F32, shape, "res_out"), HQ_OUT_F32 if f32 else HQ_OUT_BF16, T, H, post,
-          _dense(post_w, dev, _F32, vector, "post_w"), _dense(post_b, dev, _F32, vector, "post_b"), pg, gate_rows,
-          alpha, beta, pre, _dense(pre_w, dev, _F32, vector, "pre_w"), _dense(pre_b, dev, _F32, vector, "pre_b"), eps,
-          _dense(h, dev, _BF16, shape, "h"), pq, ldq, _dense(q_scale, dev, _F32, (T,), "q_scale"))
+          _dense(res_out, dev, _BF16_F32, shape, "res_out"), HQ_OUT_F32 if f32 else HQ_OUT_BF16, _int(T, "T"), _int(H, "H"),
+          _int(post, "post"), _dense(post_w, dev, _F32, vector, "post_w"), _dense(post_b, dev, _F32, vector, "post_b"), pg,
+          _int(gate_rows, "T / G"), alpha, beta, _int(pre, "pre"), _dense(pre_w, dev, _F32, vector, "pre_w"),
+          _dense(pre_b, dev, _F32, vector, "pre_b"), eps, _dense(h, dev, _BF16, shape, "h"), pq, ldq,
+          _dense(q_scale, dev, _F32, (T,), "q_scale"))
 
 
 def hq_selftest_bounded_wait(limit_cycles: int, stream=None, device=None) -> None:

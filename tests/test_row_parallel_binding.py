@@ -67,3 +67,97 @@ def test_a_module_of_another_torch_is_not_used(tmp_path):
 
 def test_the_built_module_loads(tmp_path):
     assert import_copy(tmp_path, os.path.join(ROOT, NAME, "_hqargs.so")).startswith("0 built")
+
+
+# -------------------------------------------------------------------------------- sizes past an int
+def cuda_tensor(shape, dtype, stride=None):
+    """A tensor that says it lies on a GPU, of any size, without memory: the binding's own view of it."""
+    import torch
+
+    dense = stride is None
+
+    class OnGpu(torch.Tensor):
+        def data_ptr(self):
+            return 0x10000
+
+        def is_contiguous(self):
+            return dense
+
+        def get_device(self):
+            return 0
+
+        __torch_function__ = torch._C._disabled_torch_function_impl
+
+        @classmethod
+        def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+            raise NotImplementedError(func)
+
+    if dense:
+        stride, n = [], 1
+        for d in reversed(shape):
+            stride.insert(0, n)
+            n *= d
+    return torch.Tensor._make_wrapper_subclass(OnGpu, shape, strides=stride, dtype=dtype, device="cuda:0")
+
+
+BIG = 1 << 32
+
+
+def past_an_int():
+    import torch
+
+    import bit_tensor_activation_b200 as hq
+
+    bf, i8, f32, i32, u8 = torch.bfloat16, torch.int8, torch.float32, torch.int32, torch.uint8
+    t = cuda_tensor
+
+    def product(P=1, T=4, H=64, K=64, lda=None, ldo=None):
+        lda, ldo = lda or K, ldo or H
+        return lambda: hq.hq_int8_matmul(t((P, T, K), i8, (T * lda, lda, 1)), t((P, T), f32), t((P, H, K), i8), t((P, H), f32),
+                                         t((P, T, H), bf, (T * ldo, ldo, 1)))
+
+    def tokens(rows=4, K=64, ldx=None, ldq=None):
+        return lambda: hq.hq_quantize_tokens(t((rows, K), bf, (ldx or K, 1)), t((rows, K), i8, (ldq or K, 1)), t((rows,), f32))
+
+    def pack(T=4, K=64, H=64, k=8, lda=None):
+        lda = lda or K
+        return lambda: hq.hq_int8_matmul_pack(t((1, T, K), i8, (T * lda, lda, 1)), t((1, T), f32), t((1, H, K), i8), t((1, H), f32),
+                                              t((k,), i32), t((H - k,), i32), t((1, H), f32), t((1, H), u8),
+                                              t((1, T, (H - k) // 8), i32), t((1, k, T), bf))
+
+    def norm(T=4, H=64, ldq=None, **kw):
+        x = t((T, H), bf)
+        return lambda: hq.hq_residual_norm(x, x, x, h=x, q=t((T, H), i8, (ldq or H, 1)), q_scale=t((T,), f32), **kw)
+
+    return {"as it is: tokens": (tokens(), None), "as it is: product": (product(), None), "as it is: pack": (pack(), None),
+            "as it is: norm": (norm(), None),
+            "tokens, K": (tokens(K=BIG + 64), "K|pitch"), "tokens, x's pitch": (tokens(ldx=BIG + 64), "pitch"),
+            "tokens, q's pitch": (tokens(ldq=BIG + 64), "pitch"), "product, T": (product(T=BIG + 4), "T"),
+            "product, K": (product(K=BIG + 64), "K|pitch"), "product, H": (product(H=BIG + 64), "H|pitch"),
+            "product, a's pitch": (product(lda=BIG + 64), "pitch"), "product, out's pitch": (product(ldo=BIG + 64), "pitch"),
+            "pack, T": (pack(T=BIG + 4), "T"), "pack, a's pitch": (pack(lda=BIG + 64), "pitch"),
+            "norm, T": (norm(T=BIG + 4), "T"), "norm, H": (norm(H=BIG + 64), "H|pitch"),
+            "norm, q's pitch": (norm(ldq=BIG + 64), "pitch"), "norm, post": (norm(post=BIG + 1), "post"),
+            "norm, pre": (norm(pre=BIG + 1), "pre")}
+
+
+CASES = ["as it is: tokens", "as it is: product", "as it is: pack", "as it is: norm", "tokens, K", "tokens, x's pitch",
+         "tokens, q's pitch", "product, T", "product, K", "product, H", "product, a's pitch", "product, out's pitch", "pack, T",
+         "pack, a's pitch", "norm, T", "norm, H", "norm, q's pitch", "norm, post", "norm, pre"]
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_what_an_int_does_not_hold_is_refused(case, monkeypatch):
+    """2^32 more than a size that fits is the same 32 bits: cut to them, the call would read another tensor."""
+    import bit_tensor_activation_b200 as hq
+
+    reached = []
+    monkeypatch.setattr(hq, "_call", lambda fn, where, *args: reached.append(where))
+    call, match = past_an_int()[case]
+    if match is None:
+        call()
+        assert len(reached) == 1
+        return
+    with pytest.raises(ValueError, match=match):
+        call()
+    assert not reached

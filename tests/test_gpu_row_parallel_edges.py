@@ -235,3 +235,112 @@ def test_launches_leave_pythons_lock_to_other_threads(tmp_path):
     said = dict(line.split() for line in r.stdout.splitlines() if line.startswith("hq_"))
     assert said == {n: "free" for n in ("hq_quantize_tokens", "hq_int8_matmul", "hq_int8_matmul_pack", "hq_dequant_reduce",
                                         "hq_residual_norm")}, said
+
+
+# -------------------------------------------------------------------------------- both sets of argument checks
+def calls_and_arguments():
+    """Each call that C++ and Python both check, with arguments that fit."""
+    new = lambda *s, dtype=BF: torch.ones(*s, dtype=dtype, device=DEV)  # noqa: E731
+    P, T, H, K, k = 2, 4, 64, 48, 16
+    i8, i32, u8, f32 = torch.int8, torch.int32, torch.uint8, torch.float32
+    product = dict(a=new(P, T, K, dtype=i8), a_scale=new(P, T, dtype=f32), w=new(P, H, K, dtype=i8), w_scale=new(P, H, dtype=f32))
+    wire = dict(keep_idx=torch.arange(k, dtype=i32, device=DEV), rest_idx=torch.arange(k, H, dtype=i32, device=DEV),
+                codes=new(P, T, (H - k) // 8, dtype=i32), side=new(P, k, T), zero=new(P, H, dtype=u8))
+    return {
+        "quantize_tokens": dict(x=new(T, K), q=new(T, K, dtype=i8), scale=new(T, dtype=f32), stream=None),
+        "int8_matmul": dict(**product, out=new(P, T, H), bias=new(P, H), stream=None),
+        "int8_matmul_pack": dict(**product, keep_idx=wire["keep_idx"], rest_idx=wire["rest_idx"], inv_scale=new(P, H, dtype=f32),
+                                 zero=wire["zero"], codes=wire["codes"], side=wire["side"], stream=None),
+        "dequant_reduce": dict(codes=wire["codes"], side=wire["side"], keep_idx=wire["keep_idx"], rest_idx=wire["rest_idx"],
+                               scale=new(P, H, dtype=f32), zero=wire["zero"], out=new(T, H), stream=None),
+        "residual_norm": dict(y=new(T, H), res=new(T, H), res_out=new(T, H), h=new(T, H), q=new(T, H, dtype=i8),
+                              q_scale=new(T, dtype=f32), post=1, post_w=new(H, dtype=f32), post_b=new(H, dtype=f32), gate=new(2, H),
+                              alpha=1.0, beta=1.0, pre=2, pre_w=new(H, dtype=f32), pre_b=new(H, dtype=f32), eps=1e-6, stream=None),
+    }
+
+
+def variants(n, v):
+    """Other values for argument `n`, most of which do not fit."""
+    if n == "stream":  # a number is taken for a stream's handle: only numbers that are one
+        yield from (("0", 0), ("a word", "x"), ("a stream", torch.cuda.current_stream(DEV)))
+        return
+    yield "None", None
+    yield "a number", 3
+    yield "a word", "x"
+    if not isinstance(v, torch.Tensor):
+        for x in (0, -1, 2, 5, 1.0, 0.5, True, 1e300, float("nan"), 2 ** 32 + 1, 10 ** 400, torch.tensor(1.0)):
+            yield repr(x)[:20], x
+        return
+    wide = torch.empty(*v.shape[:-1], v.shape[-1] + 16, dtype=v.dtype, device=DEV).copy_(
+        torch.nn.functional.pad(v.float(), (0, 16)).to(v.dtype))
+    odd = torch.empty(v.numel() + 1, dtype=v.dtype, device=DEV)[1:].view(v.shape).copy_(v)
+    yield "on the host", v.cpu()
+    yield "of another type", v.to(torch.float64)
+    yield "fp32", v.float()
+    yield "bf16", v.to(BF)
+    yield "int32", v.to(torch.int32)
+    if v.element_size() == 2:
+        yield "bits", v.view(torch.int16)
+        yield "unsigned bits", v.view(torch.uint16)
+    if v.dtype == torch.int32:
+        yield "unsigned", v.view(torch.uint32)
+    yield "a dimension more", v[None]
+    yield "a dimension less", v[0]
+    yield "none of it", v[:0]
+    yield "one of it", v[:1]
+    yield "one less", v[:-1]
+    yield "narrower", v[..., :-8]
+    yield "with a pitch", wide[..., :v.shape[-1]]
+    if v.dim() > 1:  # (shifted lists of features are not lists of features)
+        yield "eight further", wide[..., 8:8 + v.shape[-1]]
+    yield "misaligned", odd
+    yield "every second", torch.cat([v, v], -1)[..., ::2]
+    yield "repeated", v[:1].expand_as(v)
+    if v.is_floating_point():
+        yield "a parameter", torch.nn.Parameter(v)
+    if v.dim() > 1:
+        yield "transposed", v.transpose(0, 1)
+        yield "columns first", v.transpose(-1, -2).contiguous().transpose(-1, -2)
+    if v.dim() > 2:
+        yield "ranks interleaved", v.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+@pytest.mark.parametrize("name", ["quantize_tokens", "int8_matmul", "int8_matmul_pack", "dequant_reduce", "residual_norm"])
+def test_both_checks_take_and_refuse_the_same(name, monkeypatch):
+    """Every argument in turn in every other shape, type and place, and each pair of arguments cut to no rows:
+    what the checks in C++ call the library with, those in Python do, and the library says the same of it."""
+    public, fast = getattr(hq, "hq_" + name), getattr(hq._hqargs, name)
+
+    class Slow:
+        pass
+
+    for n in ("quantize_tokens", "int8_matmul", "int8_matmul_pack", "dequant_reduce", "residual_norm"):
+        setattr(Slow, n, staticmethod(lambda *args: None))
+    monkeypatch.setattr(hq, "_hqargs", Slow)
+    args = calls_and_arguments()[name]
+    order = {"int8_matmul": ["a", "a_scale", "w", "w_scale", "out", "bias", "stream"]}.get(name, list(args))
+
+    def both(kw, what):
+        status = fast(*(hq._handle(kw[n]) if n == "stream" else kw[n] for n in order))
+        try:
+            public(**kw)
+            other = hq.HQ_OK
+        except hq.HQError as e:
+            other = e.status
+        except Exception:
+            other = None
+        assert status == other or (status is None and other), f"{name}, {what}: {status} in C++, {other} in Python"
+        return status
+
+    assert both(args, "as it is") == hq.HQ_OK
+    seen = {both({**args, n: x}, f"{n} {what}") for n, v in args.items() for what, x in variants(n, v)}
+    assert seen >= {None, hq.HQ_OK}
+    tensors = [n for n, v in args.items() if isinstance(v, torch.Tensor)]
+    for a in tensors:
+        for b in tensors:
+            both({**args, a: args[a][:0], b: args[b][:0]}, f"{a} and {b} of no rows")
+            both({**args, a: None, b: None}, f"neither {a} nor {b}")
+    empty = {n: v[:, :0] if v.dim() > 1 and v.shape[:2] == (2, 4) else v[..., :0] if n == "side" else
+             v[:0] if v.shape[0] == 4 else v for n, v in args.items() if isinstance(v, torch.Tensor)}
+    assert both({**args, **empty}, "no rows at all") == hq.HQ_OK
+    torch.cuda.synchronize()

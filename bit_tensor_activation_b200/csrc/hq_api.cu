@@ -879,7 +879,7 @@ hq_status hq_int8_matmul_pack(const int8_t* a, int lda, const float* a_scale, co
   hq::MmArgs p{};
   p.a = a, p.lda = lda, p.a_scale = a_scale, p.w = w, p.ldw = ldw, p.w_scale = w_scale;
   p.P = P, p.T = T, p.H = H, p.K = K;
-  p.k = k, p.rest_idx = rest_idx, p.inv_scale = inv_scale, p.zero = zero, p.codes = codes, p.side = side;
+  p.k = k, p.keep_idx = keep_idx, p.rest_idx = rest_idx, p.inv_scale = inv_scale, p.zero = zero, p.codes = codes, p.side = side;
   return launch_matmul<hq::kMmWire>(p, (cudaStream_t)stream);
 }
 

@@ -24,6 +24,7 @@ struct MmArgs {
   int ldo;
   // the wire
   int k;
+  const int32_t* keep_idx;
   const int32_t* rest_idx;
   const float* inv_scale;
   const uint8_t* zero;
@@ -32,6 +33,12 @@ struct MmArgs {
 };
 
 enum MmOut { kMmBf16 = 0, kMmF32 = 1, kMmWire = 2 };
+
+// The feature, in their own order, of compact position c of the wire.
+__device__ __forceinline__ int wire_feature(const MmArgs& p, int c) {
+  const int Hr = p.H - p.k;
+  return ld_dep(c < Hr ? p.rest_idx + c : p.keep_idx + (c - Hr));
+}
 
 // ------------------------------------------------------------------------------------------------
 // Many tokens: a pair of CTAs to a tile of 256 tokens x kN features.
@@ -177,7 +184,7 @@ template <int kOut, int kN>
 struct MmFetch {
   static constexpr int kWarpChunks = MmShape<kN>::kWarpChunks, kChunks = MmShape<kN>::kChunks;
   float scale[kWarpChunks], second[kWarpChunks];
-  int rest[kWarpChunks];
+  int feature[kWarpChunks];
   uint32_t zero[kWarpChunks];
 
   __device__ __forceinline__ static int column(int n0, int j0, int i, int lane) { return n0 + 32 * (j0 + kMmSides * i) + lane; }
@@ -190,16 +197,16 @@ struct MmFetch {
       const bool on = j0 + kMmSides * i < kChunks && c < p.H;
       scale[i] = on ? ld_dep(p.w_scale + g) : 0.0f;
       second[i] = kOut != kMmWire && p.bias && on ? bf16_lo(ld_dep(p.bias + g)) : 0.0f;
-      rest[i] = kOut == kMmWire && on && c < p.H - p.k ? ld_dep(p.rest_idx + c) : 0;
+      feature[i] = kOut == kMmWire && on ? wire_feature(p, c) : 0;
       zero[i] = 0;
     }
   }
-  // The wire's grids, once the features are known.
+  // The wire's grids, once the features are known.  A kept one has none: its index is checked.
   __device__ __forceinline__ void grids(const MmArgs& p, int r, int n0, int j0, int lane) {
 #pragma unroll
     for (int i = 0; i < kWarpChunks; ++i) {
+      const size_t g = (size_t)r * p.H + checked_index(feature[i], p.H);
       if (j0 + kMmSides * i >= kChunks || column(n0, j0, i, lane) >= p.H - p.k) continue;
-      const size_t g = (size_t)r * p.H + checked_index(rest[i], p.H);
       second[i] = ld_dep(p.inv_scale + g);
       zero[i] = ld_dep(p.zero + g);
     }
@@ -526,10 +533,12 @@ struct FewFeature {
     const size_t g = (size_t)r * p.H + n;
     scale = ld_dep(p.w_scale + g);
     if (kOut != kMmWire && p.bias) second = bf16_lo(ld_dep(p.bias + g));
-    if (kOut == kMmWire && n < p.H - p.k) {
-      const size_t h = (size_t)r * p.H + checked_index(ld_dep(p.rest_idx + n), p.H);
-      second = ld_dep(p.inv_scale + h);
-      zero = ld_dep(p.zero + h);
+    if (kOut == kMmWire) {
+      const size_t h = (size_t)r * p.H + checked_index(wire_feature(p, n), p.H);
+      if (n < p.H - p.k) {  // a kept feature has no grid
+        second = ld_dep(p.inv_scale + h);
+        zero = ld_dep(p.zero + h);
+      }
     }
   }
 

@@ -156,6 +156,23 @@ def test_the_most_tokens():
     del a, a_s, codes
     torch.cuda.empty_cache()
 
+# -------------------------------------------------------------------------------- indices out of range
+@pytest.mark.parametrize("bad", [-1, 1 << 20, "H"])
+@pytest.mark.parametrize("T", [3, 40, 200])
+@pytest.mark.parametrize("kept,at", [(True, 0), (True, 23), (False, 0), (False, 500)])
+def test_an_index_out_of_range_is_reported(T, kept, at, bad):
+    """Of a kept feature as of another one."""
+    P, H, K, k = 2, 1056, 48, 24
+    _, _, _, _, wo, so, keep, rest, inv, zero = problem = wire_problem(5, P, T, H, K, k)
+    codes, side = empty_wire(P, T, H, k)
+    call = lambda: hq.hq_int8_matmul_pack(problem[0], problem[1], wo, so, keep, rest, inv, zero, codes, side)  # noqa: E731
+    call()
+    assert_no_device_error()
+    (keep if kept else rest)[at] = H if bad == "H" else bad
+    call()
+    assert hq.hq_read_device_error() == hq.HQ_ERR_BAD_INDEX
+
+
 # -------------------------------------------------------------------------------- again and again
 @pytest.mark.parametrize("P,T,H,K,k,F", [(7, 1200, 280, 208, 0, 64), (3, 20, 1112, 272, 56, 616), (2, 700, 4104, 128, 40, 128)])
 def test_a_layer_repeats_itself_bit_for_bit(P, T, H, K, k, F):

@@ -9,7 +9,7 @@ import torch
 
 import bit_tensor_activation_b200 as hq
 from gpu_helpers import DEV, assert_no_device_error
-from test_gpu_row_parallel import BF, layer, layer_problem, operands, plain_product, same, selection
+from test_gpu_row_parallel import BF, layer, layer_problem, operands, plain_product, plain_tokens, same, selection
 
 pytestmark = pytest.mark.gpu
 
@@ -361,3 +361,69 @@ def test_both_checks_take_and_refuse_the_same(name, monkeypatch):
              v[:0] if v.shape[0] == 4 else v for n, v in args.items() if isinstance(v, torch.Tensor)}
     assert both({**args, **empty}, "no rows at all") == hq.HQ_OK
     torch.cuda.synchronize()
+
+
+# -------------------------------------------------------------------------------- behind other streams and other work
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "captured"])
+@pytest.mark.parametrize("T", [5, 50, 300])
+def test_operands_from_another_stream(T, captured):
+    """Weights and scales come from a slow stream that is joined just ahead of the product, the activations
+    from a copy and a fill ahead of the quantizer; the norm behind reads a residual of that stream too."""
+    P, H, K = 1, 528, 256
+    side = torch.cuda.Stream()
+    w, w_s = torch.zeros(P, H, K, dtype=torch.int8, device=DEV), torch.zeros(P, H, device=DEV)
+    new_w, new_s = torch.empty_like(w), torch.empty_like(w_s)
+    x, src = torch.zeros(P, T, K, dtype=BF, device=DEV), torch.empty(P, T, K, dtype=BF, device=DEV)
+    q, s = torch.empty(P, T, K, dtype=torch.int8, device=DEV), torch.empty(P, T, device=DEV)
+    out, res, new_res = torch.empty(P, T, H, dtype=BF, device=DEV), torch.zeros(T, H, dtype=BF, device=DEV), torch.empty(T, H, dtype=BF, device=DEV)
+    h, r_out = torch.empty(T, H, dtype=BF, device=DEV), torch.empty(T, H, dtype=BF, device=DEV)
+    slow = torch.randn(3000, 3000, device=DEV)
+    sink = torch.empty_like(slow)
+
+    def work():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(2):
+                torch.mm(slow, slow, out=sink)
+            w.copy_(new_w)
+            w_s.copy_(new_s)
+            ready = torch.cuda.Event()
+            ready.record(side)
+            torch.mm(slow, slow, out=sink)
+            res.copy_(new_res)
+        x.copy_(src)
+        s.zero_()
+        hq.hq_quantize_tokens(x, q, s)
+        main.wait_event(ready)
+        hq.hq_int8_matmul(q, s, w, w_s, out)
+        main.wait_stream(side)
+        hq.hq_residual_norm(out[0], res, r_out, h=h, post=hq.HQ_NORM_NONE)
+        w.zero_()
+        w_s.zero_()
+        res.zero_()
+
+    run = work
+    if captured:
+        work()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            work()
+        run = graph.replay
+    for i in range(25):
+        g = torch.Generator(device=DEV).manual_seed(i)
+        src.copy_(torch.randn(P, T, K, generator=g, device=DEV).to(BF))
+        new_w.copy_(torch.randint(-127, 128, (P, H, K), generator=g, device=DEV, dtype=torch.int8))
+        new_s.copy_(torch.rand(P, H, generator=g, device=DEV) / 4096)
+        new_res.copy_(torch.randn(T, H, generator=g, device=DEV).to(BF))
+        torch.cuda.synchronize()
+        run()
+        if i % 2:
+            run()
+        torch.cuda.synchronize()
+        codes, scales = plain_tokens(src)
+        same(q, codes, "codes")
+        want = plain_product(codes, scales, new_w, new_s).to(BF)
+        same(out, want, "out")
+        same(r_out, (new_res.float() + want[0].float()).to(BF), "residual")

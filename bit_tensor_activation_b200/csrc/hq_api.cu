@@ -604,7 +604,7 @@ hq_status launch_few(const hq::MmArgs& p, DeviceInfo& d, cudaStream_t st) {
   // four 4.6).  An SM's CTAs fill its shared memory with their rings together (8 ranks, one token, H = 8192,
   // K = 1024: four to an SM 12.7 us, three 14.7).
   const int kc = (int)ceil_div(p.K, hq::kMmK);
-  const long long token_tiles = ceil_div(p.T, kTokens), tiles = ceil_div(p.H, hq::kFewFeatures) * token_tiles * p.P;
+  const long long tiles = ceil_div(p.H, hq::kFewFeatures) * p.P;
   int split = 1, split_log2 = 0;
   auto fits = [&](int s) {
     return kc / s >= (kTokens == 32 ? 2 : 4) && (s * tiles <= d.sms || (s * tiles <= 2 * d.sms && kc / s >= 8));
@@ -615,7 +615,7 @@ hq_status launch_few(const hq::MmArgs& p, DeviceInfo& d, cudaStream_t st) {
   const int fit = (int)((kSmemPerSm / per_sm - 2560 - 4 * kTokens - red) / hq::few_stage_bytes(kTokens));
   const int stages = std::max(2, std::min({fit, hq::kFewMaxStages, (int)ceil_div(kc, split)}));
   const size_t smem = 1024 + (size_t)stages * hq::few_stage_bytes(kTokens) + red;
-  const dim3 grid((unsigned)(ceil_div(p.H, hq::kFewFeatures) * split), (unsigned)token_tiles, (unsigned)p.P);
+  const dim3 grid((unsigned)(ceil_div(p.H, hq::kFewFeatures) * split), (unsigned)p.P);
   return launch_dependent(kern, grid, hq::kFewThreads, smem, st, split, map_a, map_w, p, split_log2, stages, wait_limits());
 }
 

@@ -222,21 +222,14 @@ struct MmFetch {
 };
 
 // A warp's 32 tokens' four words of codes each (x: the lane's token's, at words): `n` words of `rows` tokens,
-// `pitch` words apart.  kWide (a token's words start on 16 bytes): one store a token.  Else through 512 bytes
+// `pitch` words apart.  kWide (a token's words start and end on 16 bytes: n is 4): one store a token.  Else through 512 bytes
 // at `stage`, four lanes to a token, since single words straight from the lanes that hold them touch 32 lines
 // with every store (8 ranks, 4096 tokens, H = 4104, K = 512: 121 us, 147 so; kWide, H = 4096: 105).
 template <bool kWide>
 __device__ __forceinline__ void store_words(uint32_t* words, int pitch, const uint32_t (&x)[4], int n, int rows,
                                             uint32_t stage, int lane) {
   if constexpr (kWide) {
-    if (lane >= rows) return;
-    if (n == 4) {
-      *reinterpret_cast<uint4*>(words) = make_uint4(x[0], x[1], x[2], x[3]);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (i < n) words[i] = x[i];
+    if (lane < rows) *reinterpret_cast<uint4*>(words) = make_uint4(x[0], x[1], x[2], x[3]);
   } else {
     __syncwarp();
     st_shared16(stage + 16 * lane, x[0], x[1], x[2], x[3]);
@@ -613,6 +606,7 @@ struct FewFeature {
   }
 };
 
+// At most kTokens tokens.
 template <int kOut, int kTokens>
 __global__ void __launch_bounds__(kFewThreads)
     int8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
@@ -629,7 +623,7 @@ __global__ void __launch_bounds__(kFewThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int split = 1 << split_log2;
   const int rank = split > 1 ? (int)cluster_ctarank() : 0;
-  const int n0 = (int)(blockIdx.x >> split_log2) * kFewFeatures, t0 = blockIdx.y * kTokens, r = blockIdx.z;
+  const int n0 = (int)(blockIdx.x >> split_log2) * kFewFeatures, r = blockIdx.y;
   const int kc = (p.K + kMmK - 1) / kMmK;
   const int c0 = (kc * rank) >> split_log2, c1 = (kc * (rank + 1)) >> split_log2;
   volatile int* abort = &s_abort;
@@ -666,7 +660,7 @@ __global__ void __launch_bounds__(kFewThreads)
         unsigned char* at = base + s * few_stage_bytes(kTokens);
         mbar_arrive_expect_tx(&s_full[s], few_stage_bytes(kTokens));
         tma_load_3d(smem_addr(at), &map_w, c * kMmK, n0, r, smem_addr(&s_full[s]));
-        tma_load_3d(smem_addr(at + kFewFeatures * kMmK), &map_a, c * kMmK, t0, r, smem_addr(&s_full[s]));
+        tma_load_3d(smem_addr(at + kFewFeatures * kMmK), &map_a, c * kMmK, 0, r, smem_addr(&s_full[s]));
         if (++s == stages) s = 0, phase ^= 1;
       }
     }
@@ -692,7 +686,7 @@ __global__ void __launch_bounds__(kFewThreads)
   bool ok = true;
   if (warp < 4) {  // ------------------------------------------------------------ epilogue
     for (int j = threadIdx.x; j < kTokens; j += 128)
-      s_scale[j] = t0 + j < p.T ? ld_dep(p.a_scale + (size_t)r * p.T + t0 + j) : 0.0f;
+      s_scale[j] = j < p.T ? ld_dep(p.a_scale + (size_t)r * p.T + j) : 0.0f;
     __syncwarp();
     named_barrier_sync(128);
     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_acc, 0, abort, lim.consumer)) && !*abort;
@@ -701,11 +695,11 @@ __global__ void __launch_bounds__(kFewThreads)
     if (ok && split == 1) {
       constexpr int kGroup = kTokens < 32 ? 8 : 32;
 #pragma unroll 1
-      for (int j = 0; j < kTokens && t0 + j < p.T; j += kGroup) {
+      for (int j = 0; j < p.T; j += kGroup) {
         uint32_t v[kGroup];
         __syncwarp();  // emit's stores are those of single lanes, tc_load takes the whole warp
         tc_load(acc + j, v);
-        feature.emit(v, t0 + j, kGroup, smem_addr(s_scale + j));
+        feature.emit(v, j, kGroup, smem_addr(s_scale + j));
       }
     } else if (ok) {
       // the columns go to the CTAs that add them up
@@ -753,7 +747,7 @@ __global__ void __launch_bounds__(kFewThreads)
           for (int i = 0; i < 8; ++i)
             if (c + i < width) v[i] += ld_shared(at + 4 * i * kFewFeatures);
         }
-        feature.emit(v, t0 + rank * width + c, min(width - c, 8), smem_addr(s_scale) + 4 * (rank * width + c));
+        feature.emit(v, rank * width + c, min(width - c, 8), smem_addr(s_scale) + 4 * (rank * width + c));
       }
     }
   }

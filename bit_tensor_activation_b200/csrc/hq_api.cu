@@ -600,8 +600,8 @@ hq_status launch_few(const hq::MmArgs& p, DeviceInfo& d, cudaStream_t st) {
   // K is shared by a cluster of CTAs until they are one to an SM (4 ranks, 32 tokens, H = 4096, K = 1024 as a
   // wire: 7.3 us with 128 CTAs, 7.7 with 256), or two with at least eight steps each (64 tokens, 8192 x 8192:
   // 15.7 us with 256 CTAs, 15.8 with 128), and as long as each has four steps (one token, H = 4096, K = 512:
-  // alone 3.0 us, two to a cluster 3.4, four 3.7; up to 32 tokens two steps: H = 2048, K = 1024 4.1 us, with
-  // four 4.6).  An SM's CTAs fill its shared memory with their rings together (8 ranks, one token, H = 8192,
+  // alone 3.0 us, two to a cluster 3.4, four 3.7) or, with 17 to 32 tokens, two (measured at one shape: H = 2048,
+  // K = 1024 4.1 us, with four 4.6).  An SM's CTAs fill its shared memory with their rings together (8 ranks, one token, H = 8192,
   // K = 1024: four to an SM 12.7 us, three 14.7).
   const int kc = (int)ceil_div(p.K, hq::kMmK);
   const long long tiles = ceil_div(p.H, hq::kFewFeatures) * p.P;
@@ -674,7 +674,8 @@ hq_status launch_norm(const hq::NormArgs& a, DeviceInfo& d, cudaStream_t st) {
   auto threads = [&](int nv) { return (int)(32 * ceil_div(ceil_div(nvec, nv), 32)); };
   // Which kernel, by what was measured (bf16, gate, both weights): the row ring from 4096 < H <= 8192 and
   // eight rows an SM on (8192 x 8192: 99 us, a CTA a row 120; 1500 x 8192: 25.6 and 26.1; 777 x 8192: 16.9
-  // and 16.1; 4096 x 4096: 33.4 and 32.0); below two rows an SM one vector a thread (148 x 8192: 5.2 us,
+  // and 16.1; 4096 x 4096: 33.4 and 32.0), without biases, which have no registers there (8192 x 8192 with a layer
+  // norm's two biases, a CTA a row: 158 us); below two rows an SM one vector a thread (148 x 8192: 5.2 us,
   // two vectors 5.5; 300 x 8192: 11.9 and 9.1).
   if (nvec > hq::kRowsThreads && nvec <= hq::kRowsVec * hq::kRowsThreads && !a.post_b && !a.pre_b && a.T >= 8 * d.sms) {
     const int nt = threads(hq::kRowsVec);
@@ -686,6 +687,8 @@ hq_status launch_norm(const hq::NormArgs& a, DeviceInfo& d, cudaStream_t st) {
       return HQ_ERR_CUDA;
     return launch_dependent(kern, dim3((unsigned)d.sms), nt, stages * row, st, 1, a, stages, wait_limits());
   }
+  // Above 16384 elements a thread's 64 registers do not hold its four vectors of y, r and v: 160 to 408 bytes of
+  // them go through local memory (4096 x 32768: 309 us, 3.5 TB/s; 4096 x 16384, with 512 threads: 144, 3.7).
   if (nvec > 2 * hq::kRowMaxThreads)
     return launch_dependent(hq::residual_norm_kernel<Y, R, 4, 1024, false>, rows, threads(4), 0, st, 1, a);
   if (nvec > hq::kRowMaxThreads)

@@ -50,10 +50,13 @@ __device__ __forceinline__ int wire_feature(const MmArgs& p, int c) {
 // runs under the products of the next.  One cluster a pair of SMs walks the tiles, rank by rank.
 //
 // What bounds it.  With long K the tensor cores under the power limit: 8 ranks, 4096 tokens, H = 4096, K = 2048
-// take 171 us from cold, 3.2 POP/s, and 218 us back to back at 1000 W; the products alone, on operands that
-// stay in shared memory, reach 4.2 POP/s, 4.4 on zeros.  With K = 1024 and below the epilogue: 32768 values a
-// CTA and tile, 7 instructions each for bf16 and 14 for the wire, 2.5 and 3.8 us; K = 512, H = 4096 takes
-// 69 and 106 us.  Hence codes without conversions (wire_word), stores by TMA from 2 KB a warp (32-byte stores
+// take 182 us from cold, 3.0 POP/s, and 208 to 221 us back to back at 1000 W; the products alone, on operands
+// that stay in shared memory, reach 4.2 POP/s, 4.4 on zeros.  With K = 1024 and below the epilogue: 32768 values
+// a CTA and tile take 2.5 us as bf16 and 3.9 as the wire; K = 512, H = 4096 takes 71 and 109 us.  It is latency
+// more than instructions: their 7 and 14 a value are 0.9 and 1.8 us of issue slots, and with K = 1024 the
+// wire uses 41% of the slots, 40% of the ALU and 48% of shared memory's.  A warp waits for its chunk's load
+// from tensor memory before the chunk's arithmetic, and three such warps a scheduler do not hide that.
+// What helped: codes without conversions (wire_word), stores by TMA from 2 KB a warp (32-byte stores
 // straight from registers: 10% more time), a body small enough to stay in the instruction cache (unrolled over
 // a tile's columns: 20% more), and twelve warps (eight: 5% more for the wire; sixteen: spills).
 //
@@ -500,8 +503,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 // each and their int32 sums meet in distributed shared memory: CTA q adds up the columns q kTokens / S ..
 // of all S of them.  Sums of integers do not depend on the order.
 //
-// Weights from memory, 8 ranks, H = 8192, K = 1024: 12.7 us with one token and 13.7 with 32, 5.3 and 4.9 TB/s
-// of weights; one rank, H = 4096, K = 512, one token: 3.0 us, of which the weights' bytes are 0.3.
+// Weights from memory, 8 ranks, H = 8192, K = 1024: 12.8 us with one token and 13.6 with 32, 5.2 and 4.9 TB/s
+// of weights; one rank, H = 4096, K = 512, one token: 3.1 us, of which the weights' bytes are 0.3.  As a wire, 4
+// ranks, 32 tokens, H = 4096, K = 1024: 7.6 us, of which the weights' bytes are 2.6; the rest is set-up, eight steps
+// in a row on one CTA an SM, and an epilogue that nothing runs beside.
 //
 // Warps 0-3 are the epilogue, warp 4 loads, warp 5 issues the products.
 constexpr int kFewFeatures = 128;

@@ -184,9 +184,10 @@ class HybridAllReduce:
 
     def pack_product(self, a: torch.Tensor, a_scale: torch.Tensor, weights: "WireWeights", stream=None):
         """pack of the partial sum a [T, K] int8 (a_scale [T]) times this rank's weights, with no partial
-        sum in memory: the wire, bit for bit, of pack(hq_int8_matmul(...))."""
+        sum in memory: the wire, bit for bit, of pack(hq_int8_matmul(...)).  For ``reduce_scatter`` it is a
+        call a row block, each of which reads all of the weights."""
         p, P = self.p, self.p.P
-        blocks = 1 if self.scheme == "allgather" else P  # a call a row block: all of them take the same weights
+        blocks = 1 if self.scheme == "allgather" else P
         rows = self.T // blocks
         for j in range(blocks):
             t = slice(j * rows, (j + 1) * rows)

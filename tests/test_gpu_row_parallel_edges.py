@@ -9,7 +9,7 @@ import torch
 
 import bit_tensor_activation_b200 as hq
 from gpu_helpers import DEV, assert_no_device_error
-from test_gpu_row_parallel import BF, layer, layer_problem, operands, plain_product, plain_tokens, same, selection
+from test_gpu_row_parallel import BF, expected_layer, layer, layer_problem, operands, plain_product, plain_tokens, same, selection
 
 pytestmark = pytest.mark.gpu
 
@@ -427,3 +427,58 @@ def test_operands_from_another_stream(T, captured):
         want = plain_product(codes, scales, new_w, new_s).to(BF)
         same(out, want, "out")
         same(r_out, (new_res.float() + want[0].float()).to(BF), "residual")
+
+
+def test_calls_through_the_checks_in_python(monkeypatch):
+    """A layer, and a norm and a product with every optional argument, give the same bits without the C++ module."""
+    args = layer_problem(41, 3, 40, 528, 144, 16, 264)[0]
+    y, res, w, b = args[4], args[4].float(), torch.rand(528, device=DEV), torch.rand(528, device=DEV)
+    gate, bias = torch.randn(4, 528, device=DEV).to(BF), torch.randn(3, 528, device=DEV).to(BF)
+    a, a_s, ww, ws = operands(42, 3, 40, 528, 144)
+    results = []
+    for slow in (False, True):
+        if slow:
+            monkeypatch.setattr(hq, "_hqargs", hq._NoArgs)
+        for n in ("sum", "res", "q", "q_s", "up", "codes", "side"):
+            args[-1][n].fill_(3)
+        layer(*args)
+        out, h = torch.empty_like(res), torch.empty_like(y)
+        q, q_s = torch.empty(40, 528, dtype=torch.int8, device=DEV), torch.empty(40, device=DEV)
+        hq.hq_residual_norm(y, res, out, h=h, q=q, q_scale=q_s, post=hq.HQ_NORM_LAYER, post_w=w, post_b=b, gate=gate, alpha=0.5,
+                            beta=2.0, pre=hq.HQ_NORM_RMS, pre_w=b, pre_b=w, eps=1e-3)
+        part = torch.empty(3, 40, 528, device=DEV)
+        hq.hq_int8_matmul(a, a_s, ww, ws, part, bias=bias)
+        torch.cuda.synchronize()
+        results.append([args[-1][n].clone() for n in ("sum", "res", "q", "q_s", "up", "codes", "side")] + [out, h, q, q_s, part])
+    for i, (x, z) in enumerate(zip(*results)):
+        same(z, x, f"output {i}")
+
+
+def test_threads_that_call_at_once():
+    """Four threads, each with a stream and a problem of its own, that reach several kernels for the first time
+    together."""
+    import threading
+
+    problems = [layer_problem(50 + i, *sizes) for i, sizes in enumerate(
+        [(2, 40, 1040, 256, 32, 136), (3, 130, 528, 144, 16, 264), (1, 7, 2064, 320, 0, 72), (2, 300, 272, 64, 16, 520)])]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(args):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    layer(*args)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(p[0],)) for p in problems]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for args, natural in problems:
+        same(args[-1]["sum"], expected_layer(args, natural), "the ranks' sum")
+        same(args[-1]["up"], plain_product(args[-1]["q"][None], args[-1]["q_s"][None], args[5], args[6]).to(BF), "next projection")
